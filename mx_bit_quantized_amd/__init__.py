@@ -16,6 +16,9 @@ Names mirror the C ABI without its ``mxq_`` prefix:
     qlinear_workspace_bytes(mode, M, K)
     qlinear(policy, expert, block, x, w_codes, w_scales, bias=None, epilogue=EPI_NONE)
     qlinear_noalloc(policy, expert, block, x, w_codes, w_scales, y, bias=None, epilogue=EPI_NONE)
+
+The operators around the linears (include/mxq_block.h: norm_quantize, gemm_residual, gemm_gated)
+are in block.py and offered here under the same names.
 """
 
 import ctypes
@@ -665,3 +668,9 @@ def lowrank_up(y_pre, t, l2, epilogue=EPI_NONE, y=None, stream=None):
                                _dev_ptr(y, "y", torch.bfloat16), _stream_handle(stream))
     _check(st, "lowrank_up")
     return y
+
+
+# ------------------------------------------------- around the linears ----
+
+from .block import (GATED_GELU_TANH, GATED_SILU, NORM_LAYER, NORM_MAX_K, NORM_NONE, NORM_RMS,  # noqa: E402,F401
+                    block_kernel_name, gemm_gated, gemm_residual, norm_quantize, quantize_weight_gated_mxfp4)

@@ -25,7 +25,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 DEVICE_SOURCES = ["mxq_api.cpp", "mxq_quant.hip", "mxq_gemm.hip", "mxq_select.hip", "mxq_lowrank.hip",
-                  "mxq_layout.hip", "mxq_noalloc.hip", "mxq_check.hip"]
+                  "mxq_layout.hip", "mxq_noalloc.hip", "mxq_check.hip", "mxq_block_api.cpp", "mxq_norm.hip",
+                  "mxq_tokens.hip"]
 
 COMMON_FLAGS = [
     "-O3",

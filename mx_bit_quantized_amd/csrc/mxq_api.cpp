@@ -17,54 +17,18 @@
 #include <vector>
 
 #include "mxq.h"
+#include "mxq_host.h"
 #include "mxq_internal.h"
 
-namespace {
+using namespace mxq;
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
+namespace {
 
 struct Policy {
   int32_t n_experts;
   int32_t n_blocks;
   std::vector<uint8_t> modes;
 };
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool log_enabled() {
-  static const int on = [] {
-    const char* v = getenv("MXQ_LOG");
-    return (v != nullptr && v[0] != '\0' && v[0] != '0') ? 1 : 0;
-  }();
-  return on != 0;
-}
-
-int check_mk(int64_t rows, int64_t K, int64_t ld) {
-  if (rows < 0 || K <= 0 || ld < 0) return MXQ_ERR_SHAPE;
-  if (K % 32 != 0 || ld < K) return MXQ_ERR_SHAPE;
-  if (rows >= kMaxDim || K >= kMaxDim || ld >= kMaxDim) return MXQ_ERR_SHAPE;
-  return MXQ_OK;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
-
-// MXQ_CHECK_FINITE: scan a bf16 [rows][ld] input (or output) for infinities and
-// NaNs; MXQ_OK when the guard is off.
-int finite_guard(const char* what, const void* x, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream) {
-  if (!mxq::check_finite_enabled()) return MXQ_OK;
-  bool bad = false;
-  if (mxq::scan_nonfinite_bf16(x, rows, cols, ld, stream, &bad) != 0) return MXQ_ERR_HIP;
-  if (!bad) return MXQ_OK;
-  if (log_enabled()) fprintf(stderr, "[mxq] non-finite value in %s [%lld x %lld]\n", what, (long long)rows,
-                             (long long)cols);
-  return MXQ_ERR_NONFINITE;
-}
-
-// a launch's status, then the guard on its bf16 output
-int output_guard(hipError_t e, const char* what, const void* y, int64_t rows, int64_t cols, hipStream_t stream) {
-  if (e != hipSuccess) return MXQ_ERR_HIP;
-  return finite_guard(what, y, rows, cols, cols, stream);
-}
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

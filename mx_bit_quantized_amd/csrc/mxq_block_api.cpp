@@ -1,0 +1,147 @@
+// mxq_block_api.cpp - the extern "C" boundary of the operators around the
+// quantized linears (declared in include/mxq_block.h): validation on the host,
+// before anything is enqueued, then dispatch to the gfx950 kernels.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "mxq_block.h"
+#include "mxq_host.h"
+#include "mxq_internal.h"
+
+using namespace mxq;
+
+namespace {
+
+bool aligned16_or_null(const void* p) { return p == nullptr || aligned16(p); }
+
+// A call's modulation vectors of length n: element type, stride and grouping.
+int check_modulation(int mod_type, int64_t ld_mod, int64_t rows_per_group, int64_t n) {
+  if (mod_type != MXQ_MOD_F32 && mod_type != MXQ_MOD_BF16) return MXQ_ERR_MODE;
+  if (ld_mod < n || ld_mod >= kMaxDim || rows_per_group < 0 || rows_per_group >= kMaxDim) return MXQ_ERR_SHAPE;
+  return MXQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mxq_norm_quantize(int mode, const mxq_norm_args* args, hipStream_t stream) {
+  if (mode != MXQ_W4A4 && mode != MXQ_W4A8 && mode != MXQ_POLICY_BF16 && mode != MXQ_POLICY_TRANSFORM_ON)
+    return MXQ_ERR_MODE;
+  if (args == nullptr) return MXQ_ERR_NULL;
+  const mxq_norm_args& a = *args;
+  if (a.norm != MXQ_NORM_RMS && a.norm != MXQ_NORM_LAYER) return MXQ_ERR_MODE;
+  if (a.post_norm != MXQ_NORM_NONE && a.post_norm != MXQ_NORM_RMS && a.post_norm != MXQ_NORM_LAYER) return MXQ_ERR_MODE;
+  if (!(a.eps > 0.0f) || !isfinite(a.eps) || !isfinite(a.branch_scale)) return MXQ_ERR_MODE;
+  int st = check_mk(a.M, a.K, a.ldx);
+  if (st != MXQ_OK) return st;
+  if (a.K > MXQ_NORM_MAX_K || (mode == MXQ_POLICY_TRANSFORM_ON && a.K % 128 != 0)) return MXQ_ERR_SHAPE;
+  if (a.branch != nullptr && (st = check_mk(a.M, a.K, a.ldb)) != MXQ_OK) return st;
+  if (a.h != nullptr && (st = check_mk(a.M, a.K, a.ldh)) != MXQ_OK) return st;
+  const bool modulated = a.gate != nullptr || a.scale != nullptr || a.shift != nullptr;
+  if (modulated && (st = check_modulation(a.mod_type, a.ld_mod, a.rows_per_group, a.K)) != MXQ_OK) return st;
+  if (a.M == 0) return MXQ_OK;
+  if (a.x == nullptr || a.out == nullptr) return MXQ_ERR_NULL;
+  if (mode != MXQ_POLICY_BF16 && a.out_scales == nullptr) return MXQ_ERR_NULL;
+  if (mode == MXQ_POLICY_TRANSFORM_ON && a.act_mult == nullptr) return MXQ_ERR_NULL;
+  if (a.branch == nullptr &&
+      (a.gate != nullptr || a.post_norm != MXQ_NORM_NONE || a.branch_scale != 1.0f || a.h != nullptr))
+    return MXQ_ERR_NULL;
+  if (a.post_norm == MXQ_NORM_NONE && (a.post_weight != nullptr || a.post_bias != nullptr)) return MXQ_ERR_MODE;
+  for (const void* p : {a.x, a.branch, a.gate, a.post_weight, a.post_bias, a.weight, a.bias, a.scale, a.shift,
+                        (const void*)a.act_mult, (const void*)a.h, (const void*)a.out, (const void*)a.out_scales})
+    if (!aligned16_or_null(p)) return MXQ_ERR_ALIGN;
+  if (a.ldx % 8 != 0 || (a.branch != nullptr && a.ldb % 8 != 0) || (a.h != nullptr && a.ldh % 8 != 0) ||
+      (modulated && a.ld_mod % 8 != 0))
+    return MXQ_ERR_ALIGN;
+  if (log_enabled())
+    fprintf(stderr, "[mxq] norm_quantize mode=%d norm=%d post=%d M=%lld K=%lld\n", mode, a.norm, a.post_norm,
+            (long long)a.M, (long long)a.K);
+  if ((st = finite_guard("norm input", a.x, a.M, a.K, a.ldx, stream)) != MXQ_OK) return st;
+  if (a.branch != nullptr && (st = finite_guard("branch", a.branch, a.M, a.K, a.ldb, stream)) != MXQ_OK) return st;
+  st = hip_status(launch_norm_quant(mode, a, stream));
+  if (st != MXQ_OK) return st;
+  if (a.h != nullptr && (st = finite_guard("residual stream", a.h, a.M, a.K, a.ldh, stream)) != MXQ_OK) return st;
+  return mode == MXQ_POLICY_BF16 ? finite_guard("norm output", a.out, a.M, a.K, a.K, stream) : MXQ_OK;
+}
+
+int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
+                      const void* bias, int epilogue, const void* residual, const void* gate, int mod_type,
+                      int64_t ld_mod, int64_t rows_per_group, void* y, int64_t M, int64_t N, int64_t K,
+                      hipStream_t stream) {
+  if (mode != MXQ_W4A4 && mode != MXQ_W4A8) return MXQ_ERR_MODE;
+  if (epilogue != MXQ_EPI_NONE && epilogue != MXQ_EPI_GELU_TANH) return MXQ_ERR_MODE;
+  int st = check_mk(M, K, K);
+  if (st != MXQ_OK) return st;
+  if (N < 0 || N >= kMaxDim) return MXQ_ERR_SHAPE;
+  if (gate != nullptr && (st = check_modulation(mod_type, ld_mod, rows_per_group, N)) != MXQ_OK) return st;
+  if (M == 0 || N == 0) return MXQ_OK;
+  if (a_codes == nullptr || a_scales == nullptr || w_codes == nullptr || w_scales == nullptr || residual == nullptr ||
+      y == nullptr)
+    return MXQ_ERR_NULL;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
+      !aligned16_or_null(bias) || !aligned16(residual) || !aligned16_or_null(gate) || !aligned16(y))
+    return MXQ_ERR_ALIGN;
+  if (log_enabled())
+    fprintf(stderr, "[mxq] gemm_residual %s M=%lld N=%lld K=%lld epi=%d kernel=%s\n", mode == MXQ_W4A4 ? "w4a4" : "w4a8",
+            (long long)M, (long long)N, (long long)K, epilogue, mxq_block_kernel_name(mode, 0, 0, M, N, K));
+  if ((st = finite_guard("residual", residual, M, N, N, stream)) != MXQ_OK) return st;
+  ResidualEpi e{residual, gate, ld_mod, rows_per_group, mod_type == MXQ_MOD_BF16};
+  return output_guard(launch_tokens_residual(mode, a_codes, a_scales, w_codes, w_scales, bias, epilogue, e, y, M, N, K,
+                                             stream),
+                      "output", y, M, N, stream);
+}
+
+int mxq_quantize_weight_gated_mxfp4(const void* w_gate, const void* w_up, int64_t H, int64_t K, int64_t ldw,
+                                    void* codes, void* scales, hipStream_t stream) {
+  int st = check_mk(H, K, ldw);
+  if (st != MXQ_OK) return st;
+  if (H % 32 != 0) return MXQ_ERR_SHAPE;
+  if (H == 0) return MXQ_OK;
+  if (w_gate == nullptr || w_up == nullptr || codes == nullptr || scales == nullptr) return MXQ_ERR_NULL;
+  if (!aligned16(w_gate) || !aligned16(w_up) || !aligned16(codes) || !aligned16(scales) || ldw % 8 != 0)
+    return MXQ_ERR_ALIGN;
+  if (log_enabled()) fprintf(stderr, "[mxq] quantize_weight_gated_mxfp4 H=%lld K=%lld\n", (long long)H, (long long)K);
+  if ((st = finite_guard("gate weight", w_gate, H, K, ldw, stream)) != MXQ_OK) return st;
+  if ((st = finite_guard("up weight", w_up, H, K, ldw, stream)) != MXQ_OK) return st;
+  return hip_status(launch_mxfp4_quant_gated(w_gate, w_up, H, K, ldw, codes, scales, stream));
+}
+
+int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
+                   const void* bias_gate, const void* bias_up, int act, void* y, void* y_scales, int64_t M, int64_t H,
+                   int64_t K, hipStream_t stream) {
+  if (mode != MXQ_W4A4 && mode != MXQ_W4A8) return MXQ_ERR_MODE;
+  if (act != MXQ_GATED_SILU && act != MXQ_GATED_GELU_TANH) return MXQ_ERR_MODE;
+  if (y_scales != nullptr && mode != MXQ_W4A4) return MXQ_ERR_MODE;
+  int st = check_mk(M, K, K);
+  if (st != MXQ_OK) return st;
+  if (H < 0 || H >= kMaxDim / 2 || H % 32 != 0) return MXQ_ERR_SHAPE;
+  if (M == 0 || H == 0) return MXQ_OK;
+  if (a_codes == nullptr || a_scales == nullptr || w_codes == nullptr || w_scales == nullptr || y == nullptr)
+    return MXQ_ERR_NULL;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
+      !aligned16_or_null(bias_gate) || !aligned16_or_null(bias_up) || !aligned16(y) || !aligned16_or_null(y_scales))
+    return MXQ_ERR_ALIGN;
+  if (log_enabled())
+    fprintf(stderr, "[mxq] gemm_gated %s%s M=%lld H=%lld K=%lld act=%d kernel=%s\n", mode == MXQ_W4A4 ? "w4a4" : "w4a8",
+            y_scales != nullptr ? " -> mxfp4" : "", (long long)M, (long long)H, (long long)K, act,
+            mxq_block_kernel_name(mode, 1, y_scales != nullptr, M, H, K));
+  const hipError_t e = launch_tokens_gated(mode, a_codes, a_scales, w_codes, w_scales, bias_gate, bias_up, act, y,
+                                           y_scales, M, H, K, stream);
+  if (y_scales != nullptr) return hip_status(e);  // MXFP4 output: always finite
+  return output_guard(e, "output", y, M, H, stream);
+}
+
+const char* mxq_block_kernel_name(int mode, int gated, int mxfp4_out, int64_t M, int64_t N, int64_t K) {
+  (void)gated;
+  (void)mxfp4_out;
+  (void)M;
+  (void)N;
+  (void)K;
+  if (mode != MXQ_W4A4 && mode != MXQ_W4A8) return "invalid";
+  return mode == MXQ_W4A4 ? "tokens_w4a4" : "tokens_w4a8";
+}
+
+}  // extern "C"

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mxq_block.h"
+
 namespace mxq {
 
 // MXFP4 quantizer; `weight` selects the kernel instance that offline weight
@@ -86,6 +88,30 @@ hipError_t launch_gemm_lowrank(const void* a_codes, const void* a_scales, const 
                                const void* w_scales, const void* bias, const void* t, const void* l2, int64_t r,
                                int epilogue, void* y, void* y_scales, int64_t M, int64_t N, int64_t K,
                                hipStream_t s);
+
+// Operators around the linears (include/mxq_block.h).
+hipError_t launch_norm_quant(int mode, const mxq_norm_args& args, hipStream_t s);
+
+// The residual epilogue's operands: y = RN_bf16(residual + gate * v),
+// row m with gate vector m / rows_per_group (0: one for all rows), gate null: 1.
+struct ResidualEpi {
+  const void* residual;
+  const void* gate;
+  int64_t ld_mod, rows_per_group;
+  int mod_bf16;
+};
+
+// Few rows, and shapes outside the pipelined kernel's (mode 0 = W4A4, 1 = W4A8).
+hipError_t launch_tokens_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes,
+                                  const void* w_scales, const void* bias, int epilogue, const ResidualEpi& e, void* y,
+                                  int64_t M, int64_t N, int64_t K, hipStream_t s);
+hipError_t launch_tokens_gated(int mode, const void* a_codes, const void* a_scales, const void* w_codes,
+                               const void* w_scales, const void* bias_gate, const void* bias_up, int act, void* y,
+                               void* y_scales, int64_t M, int64_t H, int64_t K, hipStream_t s);
+
+// Weight packing of a gated block's two projections, rows interleaved by 32.
+hipError_t launch_mxfp4_quant_gated(const void* w_gate, const void* w_up, int64_t H, int64_t K, int64_t ld, void* codes,
+                                    void* scales, hipStream_t s);
 
 // MXFP4 codes and scales between the library layout (code panels, group-major
 // scales) and the canonical row-major one ([rows][K/2], [rows][K/32]).

@@ -44,26 +44,6 @@ constexpr int kMxRows = 16;     // rows per wave unit
 constexpr int kMxPanels = 4;    // panels per wave unit (fewer in the last one)
 constexpr int64_t kStreamInputBytes = int64_t(256) << 20;  // the last-level (Infinity) cache
 
-// 16-byte load of 8 bf16 input elements; with NT, with the non-temporal hint
-// (inputs larger than the last-level cache, read once: see mxfp4_quant_kernel).
-template <bool NT>
-__device__ __forceinline__ uint4 load_chunk(const uint4* p) {
-  if constexpr (NT) {
-    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-    const u32x4 q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-    return make_uint4(q.x, q.y, q.z, q.w);
-  } else {
-    return *p;
-  }
-}
-
-// Max over the 4 lanes of a quad, by DPP quad permutations (lane ^ 1, lane ^ 2).
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = umax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));
-  v = umax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));
-  return v;
-}
-
 // WEIGHT only names the instance: the offline weight pack and the activation
 // quantizer run the same code, and separate symbols keep their launches apart
 // in profiles. NT loads the input with the non-temporal hint: an input larger
@@ -71,9 +51,13 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 // pass, and streaming it keeps the codes the GEMM reads next (A14B 720p,
 // 774 MB: 212 -> 195 us); a smaller input is, and loses its reuse (TI2V-5B,
 // 70 MB: 16.5 -> 17.9 us), so the launch picks by size. Same bytes either way.
-template <bool WEIGHT, bool NT>
+//
+// GATED packs two weights as one (mxq_quantize_weight_gated_mxfp4): rows 64 b ..
+// 64 b + 31 are rows 32 b .. of x and the next 32 the same rows of x2. A unit's 16
+// rows come from one of them.
+template <bool WEIGHT, bool NT, bool GATED = false>
 __global__ __launch_bounds__(64 * kQuantWaves) void mxfp4_quant_kernel(
-    const uint16_t* __restrict__ x, int64_t rows, int64_t K, int64_t ld,
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ x2, int64_t rows, int64_t K, int64_t ld,
     uint8_t* __restrict__ codes, uint32_t* __restrict__ scales) {
   const int lane = threadIdx.x & 63;
   const int64_t unit0 = (int64_t)blockIdx.x * kQuantWaves + (threadIdx.x >> 6);
@@ -90,11 +74,13 @@ __global__ __launch_bounds__(64 * kQuantWaves) void mxfp4_quant_kernel(
     // chunks is a multiple of 4 and a panel's first chunk of 16, so a whole
     // 4-lane block is in or out of range: the shuffles stay uniform per block
     const bool ch_ok = ch < chunks;
+    const uint16_t* src = GATED && (row0 & 32) != 0 ? x2 : x;
+    const int64_t src0 = GATED ? (row0 >> 6) * 32 + (row0 & 31) : row0;
     uint4 v[kMxRows];
 #pragma unroll
     for (int t = 0; t < kMxRows; ++t) {
       const int64_t row = row0 + t;
-      v[t] = row < rows && ch_ok ? load_chunk<NT>(reinterpret_cast<const uint4*>(x + row * ld) + ch)
+      v[t] = row < rows && ch_ok ? load_chunk<NT>(reinterpret_cast<const uint4*>(src + (src0 + t) * ld) + ch)
                                  : make_uint4(0, 0, 0, 0);
     }
     const int64_t w = K - 128 * (int64_t)p < 128 ? K - 128 * (int64_t)p : 128;  // panel width
@@ -124,39 +110,6 @@ __global__ __launch_bounds__(64 * kQuantWaves) void mxfp4_quant_kernel(
 // row amax (magnitude bit patterns) over the wave, derives the scale and
 // writes 8 E4M3FN codes per chunk. Longer rows take two passes: the amax,
 // then a second read of the row to quantize it.
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = umax(v, (uint32_t)__shfl_xor((int)v, off));
-  return v;
-}
-
-// Signed IEEE quotient x / s of a bf16 element: formed from |x| (rounding to
-// nearest is symmetric; the FMA correction would lose the sign of -0) with
-// x's sign attached. A row of zeros has s = 0: its quotients are signed zeros
-// (the reciprocal is infinite there, and 0 * inf would be NaN).
-__device__ __forceinline__ float fp8_signed_quotient(uint32_t bits16, const Fp8Row& r) {
-  const float q = r.s == 0.0f ? 0.0f : fp8_quotient(as_float((bits16 & 0x7FFFu) << 16), r);
-  return as_float(as_uint(q) | ((bits16 & 0x8000u) << 16));
-}
-
-// 8 bf16 -> 8 E4M3FN codes. The quotients are correctly rounded fp32 with
-// |q| <= 448 (1 + 2^-22); gfx950's packed conversion rounds them to nearest
-// even, signs and subnormals included: for every fp32 with |q| <= 464 it
-// equals e4m3fn_code (an exhaustive GPU test checks it).
-__device__ __forceinline__ uint2 pack8_fp8(const uint4 c, const Fp8Row& r) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t out[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float q0 = fp8_signed_quotient(w[2 * i] & 0xFFFFu, r), q1 = fp8_signed_quotient(w[2 * i] >> 16, r);
-    const float q2 = fp8_signed_quotient(w[2 * i + 1] & 0xFFFFu, r), q3 = fp8_signed_quotient(w[2 * i + 1] >> 16, r);
-    uint32_t o = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q0, q1, 0, false);
-    o = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q2, q3, (int)o, true);
-    out[i] = o;
-  }
-  return make_uint2(out[0], out[1]);
-}
 
 template <int MAXC>
 __global__ __launch_bounds__(64 * kQuantWaves) void fp8_quant_row_kernel(
@@ -220,83 +173,6 @@ __global__ __launch_bounds__(64 * kQuantWaves) void fp8_quant_kernel(
 // holds 1 / sqrt(128)); then rounding to bf16 and the MXFP4 rule above.
 
 constexpr uint32_t kInvSqrt128Bits = 0x3DB504F3u;  // RN(1 / sqrt(128)) in fp32
-
-// 128-point transform of one row panel held by 16 lanes, 8 elements each:
-// lane chunk c holds elements 8c .. 8c + 7. Every lane of the wave takes part
-// in the exchanges (no lane may be inactive here).
-//
-// Stages h = 1, 2, 4 run inside the lane. Stages h = 8, 16, 32, 64 pair the
-// lanes whose chunk index differs in bit 1, 2, 4, 8 (lane ^ 1, ^ 2, ^ 4, ^ 8
-// within the 16-lane row). They keep a known sign per lane: afterwards the
-// lane holds (-1)^popcount(c) times the transform (callers fold that sign
-// into the channel factor, an exact change). In that form each stage is one
-// fused multiply-add of the partner's value, read through DPP, into the
-// lane's own: with u = s v (the partner's sign equal to the lane's s before
-// the stage), the lane whose bit is clear computes u_p + u = s (a + b) and
-// keeps its sign, the other computes u - u_p = -s (a - b) and flips it. Each
-// is one rounding of a + b or a - b, up to that sign; only the sign of an
-// exact zero is lost, and callers turn every exact zero into +0.
-// The DPP patterns: lane ^ 1 and ^ 2 are quad permutations, ^ 8 the row
-// rotation by 8, ^ 4 the half-row mirror (lane ^ 7) then the quad
-// permutation lane ^ 3. All are their own inverses, so no direction
-// convention matters. A DPP read of a register needs two wait states after
-// a VALU write of it: the block opens with them, and inside it every DPP
-// source was written eight instructions earlier.
-__device__ __forceinline__ void fwht128_lanes(float (&f)[8], int c) {
-#pragma unroll
-  for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if ((e & h) == 0) {
-        const float a = f[e], b = f[e + h];
-        f[e] = a + b;
-        f[e + h] = a - b;
-      }
-  const float s1 = (c & 1) ? -1.0f : 1.0f, s2 = (c & 2) ? -1.0f : 1.0f;
-  const float s4 = (c & 4) ? -1.0f : 1.0f, s8 = (c & 8) ? -1.0f : 1.0f;
-  float t0, t1, t2, t3, t4, t5, t6, t7;
-#define MXQ_DPP_FMAC(D, S, SG, PAT) "v_fmac_f32_dpp " D ", " S ", " SG " " PAT " row_mask:0xf bank_mask:0xf bound_ctrl:1\n\t"
-#define MXQ_DPP_MOV(D, S, PAT) "v_mov_b32_dpp " D ", " S " " PAT " row_mask:0xf bank_mask:0xf bound_ctrl:1\n\t"
-#define MXQ_STAGE8(SG, PAT)                                                                                   \
-  MXQ_DPP_FMAC("%0", "%0", SG, PAT) MXQ_DPP_FMAC("%1", "%1", SG, PAT) MXQ_DPP_FMAC("%2", "%2", SG, PAT)      \
-  MXQ_DPP_FMAC("%3", "%3", SG, PAT) MXQ_DPP_FMAC("%4", "%4", SG, PAT) MXQ_DPP_FMAC("%5", "%5", SG, PAT)      \
-  MXQ_DPP_FMAC("%6", "%6", SG, PAT) MXQ_DPP_FMAC("%7", "%7", SG, PAT)
-  asm volatile(
-      "s_nop 1\n\t"
-      MXQ_STAGE8("%16", "quad_perm:[1,0,3,2]")
-      MXQ_STAGE8("%17", "quad_perm:[2,3,0,1]")
-      MXQ_DPP_MOV("%8", "%0", "row_half_mirror") MXQ_DPP_MOV("%9", "%1", "row_half_mirror")
-      MXQ_DPP_MOV("%10", "%2", "row_half_mirror") MXQ_DPP_MOV("%11", "%3", "row_half_mirror")
-      MXQ_DPP_MOV("%12", "%4", "row_half_mirror") MXQ_DPP_MOV("%13", "%5", "row_half_mirror")
-      MXQ_DPP_MOV("%14", "%6", "row_half_mirror") MXQ_DPP_MOV("%15", "%7", "row_half_mirror")
-      MXQ_DPP_FMAC("%0", "%8", "%18", "quad_perm:[3,2,1,0]") MXQ_DPP_FMAC("%1", "%9", "%18", "quad_perm:[3,2,1,0]")
-      MXQ_DPP_FMAC("%2", "%10", "%18", "quad_perm:[3,2,1,0]") MXQ_DPP_FMAC("%3", "%11", "%18", "quad_perm:[3,2,1,0]")
-      MXQ_DPP_FMAC("%4", "%12", "%18", "quad_perm:[3,2,1,0]") MXQ_DPP_FMAC("%5", "%13", "%18", "quad_perm:[3,2,1,0]")
-      MXQ_DPP_FMAC("%6", "%14", "%18", "quad_perm:[3,2,1,0]") MXQ_DPP_FMAC("%7", "%15", "%18", "quad_perm:[3,2,1,0]")
-      MXQ_STAGE8("%19", "row_ror:8")
-      : "+v"(f[0]), "+v"(f[1]), "+v"(f[2]), "+v"(f[3]), "+v"(f[4]), "+v"(f[5]), "+v"(f[6]), "+v"(f[7]),
-        "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3), "=&v"(t4), "=&v"(t5), "=&v"(t6), "=&v"(t7)
-      : "v"(s1), "v"(s2), "v"(s4), "v"(s8));
-#undef MXQ_STAGE8
-#undef MXQ_DPP_MOV
-#undef MXQ_DPP_FMAC
-}
-
-__device__ __forceinline__ void bf16x8_to_f32(const uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = as_float(w[i] << 16);
-    f[2 * i + 1] = as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t bf16x2_rne(float a, float b) {
-  const f32x2_t f = {a, b};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
-}
 
 // The MXFP4 quantizer's mapping and stores, on transformed rows: each step's
 // 16 lanes of a row panel transform their 128 elements together, apply the
@@ -561,11 +437,23 @@ hipError_t launch_mxfp4_quant(const void* x, int64_t rows, int64_t K, int64_t ld
   const dim3 grid((unsigned)blocks), block(64 * kQuantWaves);
   const bool streamed = rows * ld * 2 > kStreamInputBytes;
   if (weight)
-    hipLaunchKernelGGL((mxfp4_quant_kernel<true, false>), grid, block, 0, s, xs, rows, K, ld, cs, ss);
+    hipLaunchKernelGGL((mxfp4_quant_kernel<true, false>), grid, block, 0, s, xs, nullptr, rows, K, ld, cs, ss);
   else if (streamed)
-    hipLaunchKernelGGL((mxfp4_quant_kernel<false, true>), grid, block, 0, s, xs, rows, K, ld, cs, ss);
+    hipLaunchKernelGGL((mxfp4_quant_kernel<false, true>), grid, block, 0, s, xs, nullptr, rows, K, ld, cs, ss);
   else
-    hipLaunchKernelGGL((mxfp4_quant_kernel<false, false>), grid, block, 0, s, xs, rows, K, ld, cs, ss);
+    hipLaunchKernelGGL((mxfp4_quant_kernel<false, false>), grid, block, 0, s, xs, nullptr, rows, K, ld, cs, ss);
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_quant_gated(const void* w_gate, const void* w_up, int64_t H, int64_t K, int64_t ld, void* codes,
+                                    void* scales, hipStream_t s) {
+  const int64_t pchunks = ((K + 127) / 128 + kMxPanels - 1) / kMxPanels;
+  const int64_t units = 2 * H / kMxRows * pchunks;
+  int64_t blocks = (units + kQuantWaves - 1) / kQuantWaves;
+  if (blocks > (1 << 16)) blocks = 1 << 16;  // units loop beyond
+  hipLaunchKernelGGL((mxfp4_quant_kernel<true, false, true>), dim3((unsigned)blocks), dim3(64 * kQuantWaves), 0, s,
+                     static_cast<const uint16_t*>(w_gate), static_cast<const uint16_t*>(w_up), 2 * H, K, ld,
+                     static_cast<uint8_t*>(codes), static_cast<uint32_t*>(scales));
   return hipGetLastError();
 }
 
