@@ -89,7 +89,7 @@ int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const
             (long long)M, (long long)N, (long long)K, epilogue, mxq_block_kernel_name(mode, 0, 0, M, N, K));
   if ((st = finite_guard("residual", residual, M, N, N, stream)) != MXQ_OK) return st;
   ResidualEpi e{residual, gate, ld_mod, rows_per_group, mod_type == MXQ_MOD_BF16};
-  return output_guard(launch_tokens_residual(mode, a_codes, a_scales, w_codes, w_scales, bias, epilogue, e, y, M, N, K,
+  return output_guard(launch_gemm_residual(mode, a_codes, a_scales, w_codes, w_scales, bias, epilogue, e, y, M, N, K,
                                              stream),
                       "output", y, M, N, stream);
 }
@@ -128,19 +128,17 @@ int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const vo
     fprintf(stderr, "[mxq] gemm_gated %s%s M=%lld H=%lld K=%lld act=%d kernel=%s\n", mode == MXQ_W4A4 ? "w4a4" : "w4a8",
             y_scales != nullptr ? " -> mxfp4" : "", (long long)M, (long long)H, (long long)K, act,
             mxq_block_kernel_name(mode, 1, y_scales != nullptr, M, H, K));
-  const hipError_t e = launch_tokens_gated(mode, a_codes, a_scales, w_codes, w_scales, bias_gate, bias_up, act, y,
+  const hipError_t e = launch_gemm_gated(mode, a_codes, a_scales, w_codes, w_scales, bias_gate, bias_up, act, y,
                                            y_scales, M, H, K, stream);
   if (y_scales != nullptr) return hip_status(e);  // MXFP4 output: always finite
   return output_guard(e, "output", y, M, H, stream);
 }
 
 const char* mxq_block_kernel_name(int mode, int gated, int mxfp4_out, int64_t M, int64_t N, int64_t K) {
-  (void)gated;
-  (void)mxfp4_out;
-  (void)M;
-  (void)N;
-  (void)K;
   if (mode != MXQ_W4A4 && mode != MXQ_W4A8) return "invalid";
+  const bool pipe = gated ? gemm_gated_pipelined(mode, M, N, K, mxfp4_out != 0)
+                          : gemm_residual_pipelined(mode, M, N, K, ResidualEpi{});
+  if (pipe) return mode == MXQ_W4A4 ? "pipe_w4a4" : "pipe_w4a8";
   return mode == MXQ_W4A4 ? "tokens_w4a4" : "tokens_w4a8";
 }
 

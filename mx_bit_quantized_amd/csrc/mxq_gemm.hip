@@ -447,9 +447,57 @@ __device__ __forceinline__ float acc_read(float a) {
   return v;
 }
 
+// One value written to an accumulator register at the point of use, for the
+// same reason. (The product's next instruction on it starts from zero, and its
+// next reader is acc_read, so no MFMA wait applies.)
+__device__ __forceinline__ float acc_write(float v) {
+  float a;
+  asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(a) : "v"(v));
+  return a;
+}
+
 // Range-checked 4-byte store (one data register: no late read).
 __device__ __forceinline__ void buf_store4(const i32x4& rs, uint32_t voff, uint32_t v) {
   asm volatile("buffer_store_dword %0, %1, %2, 0 offen" :: "v"(v), "v"(voff), "s"(rs) : "memory");
+}
+
+// Range-checked 2-byte store of the low half of v.
+__device__ __forceinline__ void buf_store2(const i32x4& rs, uint32_t voff, uint32_t v) {
+  asm volatile("buffer_store_short %0, %1, %2, 0 offen" :: "v"(v), "v"(voff), "s"(rs) : "memory");
+}
+
+// E8M0 scale byte of a 32-column block of one row from the lane's 8 bf16 pairs
+// and its partner's (lane +- 32), g the lane's half.
+__device__ __forceinline__ uint32_t tile_block_scale(const uint32_t (&pk)[4][2], int g) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m2 = {0, 0};
+#pragma unroll
+  for (int t2 = 0; t2 < 4; ++t2)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(u16x2, pk[t2][h] & 0x7FFF7FFFu));
+  uint32_t am = umax((uint32_t)m2.x, (uint32_t)m2.y);
+  const auto sw = __builtin_amdgcn_permlane32_swap(am, am, false, false);
+  am = umax(am, g ? (uint32_t)sw[0] : (uint32_t)sw[1]);
+  return mx_scale_byte(am);
+}
+
+// The block's codes: 8 contiguous bytes (of the row's 16) per lane, the lower
+// lane's first. Lane g = 0 converts bytes 4 t + {0, 1}, lane g = 1 bytes 4 t + {2, 3};
+// a lane swap brings both halves' t = 0, 1 to the lower lane and t = 2, 3 to the upper.
+__device__ __forceinline__ uint2 tile_codes(const uint32_t (&pk)[4][2], uint32_t sb) {
+  const float scq = as_float(sb << 23);
+  uint32_t e0 = 0, e1 = 0;
+  e0 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e0, __builtin_bit_cast(bf16x2, pk[0][0]), scq, 0);
+  e0 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e0, __builtin_bit_cast(bf16x2, pk[0][1]), scq, 1);
+  e0 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e0, __builtin_bit_cast(bf16x2, pk[1][0]), scq, 2);
+  e0 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e0, __builtin_bit_cast(bf16x2, pk[1][1]), scq, 3);
+  e1 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e1, __builtin_bit_cast(bf16x2, pk[2][0]), scq, 0);
+  e1 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e1, __builtin_bit_cast(bf16x2, pk[2][1]), scq, 1);
+  e1 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e1, __builtin_bit_cast(bf16x2, pk[3][0]), scq, 2);
+  e1 = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e1, __builtin_bit_cast(bf16x2, pk[3][1]), scq, 3);
+  const auto pq = __builtin_amdgcn_permlane32_swap(e0, e1, false, false);
+  return make_uint2(__builtin_amdgcn_perm((uint32_t)pq[1], (uint32_t)pq[0], 0x05040100u),
+                    __builtin_amdgcn_perm((uint32_t)pq[1], (uint32_t)pq[0], 0x07060302u));
 }
 
 // Range-checked 8-byte store (no late read of its data registers).
@@ -462,6 +510,17 @@ __device__ __forceinline__ void buf_store16(const i32x4& rs, uint32_t voff, cons
   const i32x4 d = {(int)v.x, (int)v.y, (int)v.z, (int)v.w};
   asm volatile("buffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1" :: "v"(d), "v"(voff), "s"(rs) : "memory");
 }
+
+// Operators fused around the product (FUSE, below).
+constexpr int kFuseNone = 0, kFuseGated = 1, kFuseResidual = 2;
+
+struct FuseArgs {
+  const uint16_t* bias_up;   // gated: bias of the second projection
+  const uint16_t* residual;  // residual: bf16 [M][N]
+  const void* gate;          // residual: [groups][ld_mod] or null
+  int64_t ld_mod;
+  int rows_per_group, mod_bf16;
+};
 
 // QOUT: instead of y in bf16 the kernel writes the quantization of those bf16
 // values in the activation format of a next layer of the same mode.
@@ -487,7 +546,24 @@ __device__ __forceinline__ void buf_store16(const i32x4& rs, uint32_t voff, cons
 // steps of the stage read chunks {0, 2} and {1, 3} of the row, as both
 // operands do). The stage's scale copies go out of range: they write zeros
 // and read nothing, and keep the copy count of every stage the same.
-template <int MODE, int KT, int NB, bool GELU, bool BIAS, int QOUT, bool LRB, int WAVES>
+//
+// FUSE = kFuseGated: both projections of a gated feed-forward block. The weight
+// interleaves them by 32 rows, so the wave's four column tiles i = 0 .. 3 are
+// gate, up, gate, up of its two 32-column pieces of the hidden state, and a lane
+// holds gate and up of the same element in the same accumulator position: the
+// epilogue takes them tile after tile (j outer), holds act(gate) for one slot,
+// and rounds the product once. N counts weight rows; the output has N / 2 columns.
+// GELU chooses the activation (tanh-GELU, else SiLU).
+//
+// FUSE = kFuseResidual: y = residual + gate * epi(sum + bias), rounded once. After
+// a tile's code stages come four residual stages: the residual tile's bf16 columns
+// 32 q .. (the wn = 0 half) ride in the W role of stage q and columns 128 + 32 q ..
+// (wn = 1) in the X role, 64 bytes per token row, so the copies run ahead through
+// the ring like any others and no load waits in the epilogue, where its wait
+// would also drain the copies in flight (vmcnt counts them in order). In stage q
+// each wave turns its column tiles i = q into the final fp32 values in place; the
+// ordinary epilogue then only rounds and stores.
+template <int MODE, int KT, int NB, bool GELU, bool BIAS, int QOUT, bool LRB, int WAVES, int FUSE>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES / 4))) void
 gemm_pipe_kernel(
     const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws,
@@ -495,10 +571,13 @@ gemm_pipe_kernel(
     const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, uint8_t* __restrict__ y_scales,
     const float* __restrict__ out_amax, int M, int N, int K, int tiles_m, int tiles_n,
     const uint16_t* __restrict__ lr_t, const uint16_t* __restrict__ lr_l2, int lr_rank,
-    const float* __restrict__ out_mult) {
+    const float* __restrict__ out_mult, const FuseArgs fuse) {
   using C = PipeCfg<MODE, KT, NB, WAVES>;
   constexpr int TM = C::TM, NT = C::NT;
   static_assert(!LRB || (MODE == 0 && KT == 128 && WAVES == 4), "the branch stages take the shape of a W4A4 code stage");
+  static_assert(FUSE == kFuseNone || (QOUT < 2 && !LRB && (QOUT == 0 || (MODE == 0 && FUSE == kFuseGated))), "fused forms");
+  static_assert(FUSE != kFuseResidual || WAVES == 4, "residual stages: one wave per SIMD");
+  constexpr bool GATED = FUSE == kFuseGated, RES = FUSE == kFuseResidual;
   static_assert(QOUT < 2 || (MODE == 0 && WAVES == 4 && !LRB), "transformed output: W4A4, four waves");
   // ring of NB stage slots, then two tile-parameter blocks: bias slice (512
   // bytes), a sink for the unused waves' copies (512), token scales (1024, FP8)
@@ -530,7 +609,8 @@ gemm_pipe_kernel(
   const uint32_t w_row = (uint32_t)K >> 1;
   const uint32_t x_row = MODE == 0 ? ((uint32_t)K >> 1) : (uint32_t)K;
   const int nq = K / KT;                                   // code stages of a tile
-  const int n_stages = nq + (LRB ? (lr_rank >> 5) : 0);   // + the branch's rank panels
+  const int n_stages = nq + (LRB ? (lr_rank >> 5) : RES ? 4 : 0);   // + the branch's rank panels, the residual's columns
+  const int NY = GATED ? N >> 1 : N;                       // columns of the output
 
   // This workgroup's tiles: first, first + stride, ... (count of them).
   const int total = tiles_m * tiles_n;
@@ -580,6 +660,19 @@ gemm_pipe_kernel(
 #pragma unroll
     for (int q = 0; q < C::X_INSTR; ++q) vxl[q] = vx[q] / C::X_RB * lr_pitch + vx[q] % C::X_RB;
   }
+  // residual stages: 64 bytes of a token row of the output's row pitch (the FP8
+  // X role has rows of 128 bytes: its upper halves copy nothing)
+  uint32_t vwr[RES ? C::W_INSTR : 1], vxr[RES ? C::X_INSTR : 1];
+  if constexpr (RES) {
+#pragma unroll
+    for (int q = 0; q < C::W_INSTR; ++q) vwr[q] = vw[q] / C::W_RB * ((uint32_t)N * 2u) + vw[q] % C::W_RB;
+#pragma unroll
+    for (int q = 0; q < C::X_INSTR; ++q) {
+      int row, c;
+      unswz<C::X_RB>((wave * C::X_INSTR + q) * 64 + lane, row, c);
+      vxr[q] = c < 4 ? (uint32_t)row * ((uint32_t)N * 2u) + (uint32_t)c * 16u + 256u : 0x80000000u;
+    }
+  }
   const uint32_t w_panel = (uint32_t)N * C::W_RB;  // bytes of one code panel
   const uint32_t x_stage = MODE == 0 ? (uint32_t)M * C::X_RB : (uint32_t)C::X_RB;
   // Scales (group-major, 128-element groups): the tile's 256 dwords of group
@@ -627,6 +720,19 @@ gemm_pipe_kernel(
   uint32_t cp_nb, cp_mb, nx_nb, nx_mb;  // the cursor's tile and the tile after it
   tile_base(0, cp_nb, cp_mb);
   tile_base(1, nx_nb, nx_mb);
+  // residual rows of a tile (RES): address and bytes from its first row on, so
+  // that offsets stay below 2^31 for residuals of any size
+  uint32_t cp_rlo = 0, cp_rhi = 0, cp_rsz = 0, nx_rlo = 0, nx_rhi = 0, nx_rsz = 0;
+  auto residual_base = [&](uint32_t mb, uint32_t& lo, uint32_t& hi, uint32_t& size) {
+    const uint64_t a = reinterpret_cast<uint64_t>(fuse.residual) + (uint64_t)mb * (uint64_t)N * 2u;
+    lo = (uint32_t)a;
+    hi = (uint32_t)(a >> 32);
+    size = (uint32_t)min(256, M - (int)mb) * (uint32_t)N * 2u;
+  };
+  if constexpr (RES) {
+    residual_base(cp_mb, cp_rlo, cp_rhi, cp_rsz);
+    residual_base(nx_mb, nx_rlo, nx_rhi, nx_rsz);
+  }
   // Copy q (0 .. PER_WAVE-1) of the cursor's stage into ring slot `slot`.
   // Past the last tile the copies are still issued (so the wait counts stay
   // constant and the issue has no branch) but with 2^31 added to the offset,
@@ -639,13 +745,17 @@ gemm_pipe_kernel(
     constexpr uint32_t oob = 0x80000000u;
     const uint32_t base = lds_ring + (uint32_t)slot * C::STAGE;
     // a branch stage (LRB): its rank panel, and its source rows 2 r bytes apart
-    const bool br = LRB && cp_s >= nq;
+    const bool br = (LRB || RES) && cp_s >= nq;
     const uint32_t lr_off = LRB ? (uint32_t)(cp_s - nq) * 64u : 0u;
     if (q < C::W_INSTR) {
       const uint32_t so = live ? cp_nb * (uint32_t)C::W_RB + (uint32_t)cp_s * w_panel : oob;
       if constexpr (LRB) {
         const uint32_t sl = live ? cp_nb * lr_pitch + lr_off : oob;
         lds_dma16(br ? rl2 : rw, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, br ? vwl[q] + sl : vw[q] + so);
+      } else if constexpr (RES) {
+        const uint32_t sl = live ? cp_nb * 2u + (uint32_t)(cp_s - nq) * 64u : oob;
+        const i32x4 rr = {(int)cp_rlo, (int)cp_rhi, (int)cp_rsz, 0x00020000};
+        lds_dma16(br ? rr : rw, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, br ? vwr[q] + sl : vw[q] + so);
       } else {
         lds_dma16(rw, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, vw[q] + so);
       }
@@ -656,6 +766,13 @@ gemm_pipe_kernel(
       if constexpr (LRB) {
         const uint32_t sl = live ? cp_mb * lr_pitch + lr_off : oob;
         lds_dma16(br ? rlt : rx, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, br ? vxl[qx] + sl : vx[qx] + so);
+      } else if constexpr (RES) {
+        // (an offset past the end from either part keeps the top bit: their sum
+        // is formed with or, the parts being below 2^31 otherwise)
+        const uint32_t sl = live ? cp_nb * 2u + (uint32_t)(cp_s - nq) * 64u : oob;
+        const uint32_t vr = (vxr[qx] | sl) & 0x80000000u ? 0x80000000u : vxr[qx] + sl;
+        const i32x4 rr = {(int)cp_rlo, (int)cp_rhi, (int)cp_rsz, 0x00020000};
+        lds_dma16(br ? rr : rx, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, br ? vr : vx[qx] + so);
       } else {
         lds_dma16(rx, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, vx[qx] + so);
       }
@@ -663,7 +780,7 @@ gemm_pipe_kernel(
       // the offset is below 2^31, so or-ing in the top bit puts it out of range
       // (a select of the computed offset here compiles to a branch)
       const uint32_t row0 = (cp_nb & sc_w) | (cp_mb & ~sc_w);
-      const uint32_t so = (row0 * 4u + (uint32_t)cp_s * sc_group) | (live ? 0u : oob);
+      const uint32_t so = (row0 * 4u + (uint32_t)cp_s * sc_group) | (live && !br ? 0u : oob);
       lds_dma4(rsc, base + sc_lds, vs + so);
     } else if (q == C::W_INSTR + C::X_INSTR) {
       const uint32_t so = live && !br ? cp_nb * 4u + (uint32_t)(cp_s * KT / 128) * ws_group : oob;
@@ -682,6 +799,11 @@ gemm_pipe_kernel(
     const uint32_t take = 0u - (uint32_t)wrap;
     cp_nb = (nx_nb & take) | (cp_nb & ~take);
     cp_mb = (nx_mb & take) | (cp_mb & ~take);
+    if constexpr (RES) {
+      cp_rlo = (nx_rlo & take) | (cp_rlo & ~take);
+      cp_rhi = (nx_rhi & take) | (cp_rhi & ~take);
+      cp_rsz = (nx_rsz & take) | (cp_rsz & ~take);
+    }
   };
   // Tile parameters of tile k into parameter block k & 1 (issued in stage 1
   // of tile k - 1, read in the first stage of tile k + 1): the bias slice
@@ -696,9 +818,18 @@ gemm_pipe_kernel(
     if (live) tile_of(first + k * stride, tiles_m, tiles_n, tm, tn);
     const uint32_t pb = lds_ring + PARAM_OFF + (uint32_t)(k & 1) * PARAM_BYTES;
     const uint32_t nb = (uint32_t)tn * 256u, mb = (uint32_t)tm * 256u;
-    const i32x4 rb = make_rsrc(bias + nb, bias != nullptr ? ((uint32_t)N - nb) * 2u : 0u);
-    lds_dma4(rb, pb + (wave < 2 ? P_BIAS + wave * 256 : P_SINK + ((wave - 2) & 1) * 256),
-             live && wave < 2 ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
+    if constexpr (GATED) {
+      // the tile's 128 hidden columns: the gate's bias by wave 0, the up one's by wave 1
+      const uint32_t hb = nb >> 1;
+      const uint16_t* src = wave == 0 ? bias : fuse.bias_up;
+      const i32x4 rb = make_rsrc(src + hb, src != nullptr ? ((uint32_t)NY - hb) * 2u : 0u);
+      lds_dma4(rb, pb + (wave < 2 ? P_BIAS + wave * 256 : P_SINK + ((wave - 2) & 1) * 256),
+               live && wave < 2 ? (uint32_t)(lane * 4) : 0x80000000u);
+    } else {
+      const i32x4 rb = make_rsrc(bias + nb, bias != nullptr ? ((uint32_t)N - nb) * 2u : 0u);
+      lds_dma4(rb, pb + (wave < 2 ? P_BIAS + wave * 256 : P_SINK + ((wave - 2) & 1) * 256),
+               live && wave < 2 ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
+    }
     if constexpr (MODE == 1) {
       const i32x4 rt = make_rsrc(static_cast<const uint8_t*>(asc) + mb * 4u, ((uint32_t)M - mb) * 4u);
       lds_dma4(rt, pb + P_TOK + wave * 256, live ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
@@ -853,7 +984,9 @@ gemm_pipe_kernel(
   // stores and one scale store; W4A8: 32 bf16 stores, or with QOUT 2 per tile
   // pair and one store of row scales), the same whatever the shape: rows past
   // M and columns past N get an offset the range check drops.
-  constexpr int EPI_STORES = MODE == 0 ? (QOUT ? 3 * TM : WAVES == 4 ? 32 : 2 * NT) : (QOUT ? 17 : 32);
+  // (gated: two stores per 32 x 32 tile of the hidden state, or one code and one
+  // scale store per 32 rows)
+  constexpr int EPI_STORES = GATED ? (QOUT ? 2 * TM : 4 * TM) : MODE == 0 ? (QOUT ? 3 * TM : WAVES == 4 ? 32 : 2 * NT) : (QOUT ? 17 : 32);
   constexpr int EPI_OPS = EPI_STORES + EPI_PARAM_OPS;
   // Output resource of one tile's rows for the row-major outputs (bf16, or
   // static FP8 codes): its base is the tile's first row, so the offsets stay
@@ -862,8 +995,8 @@ gemm_pipe_kernel(
   constexpr uint32_t Y_ELT = MODE == 1 && QOUT ? 1u : 2u;
   auto tile_out = [&](int ptm) {
     const int rows = min(256, M - ptm * 256);
-    return make_rsrc(reinterpret_cast<const uint8_t*>(y) + (size_t)ptm * 256u * (size_t)N * Y_ELT,
-                     (uint32_t)rows * (uint32_t)N * Y_ELT);
+    return make_rsrc(reinterpret_cast<const uint8_t*>(y) + (size_t)ptm * 256u * (size_t)NY * Y_ELT,
+                     (uint32_t)rows * (uint32_t)NY * Y_ELT);
   };
   Fp8Out fo{};
   if constexpr (MODE == 1 && QOUT) fo = fp8_out_setup(*out_amax);
@@ -936,14 +1069,16 @@ gemm_pipe_kernel(
             v0 = acc[i][j][4 * t2 + 2 * h];
             v1 = acc[i][j][4 * t2 + 2 * h + 1];
           }
-          if constexpr (MODE == 1) {
+          if constexpr (RES) {
+            // final values already (the residual stages)
+          } else if constexpr (MODE == 1) {
             v0 = BIAS ? __builtin_fmaf(v0, sm, b[4 * t2 + 2 * h]) : v0 * sm;
             v1 = BIAS ? __builtin_fmaf(v1, sm, b[4 * t2 + 2 * h + 1]) : v1 * sm;
           } else if constexpr (BIAS) {
             v0 += b[4 * t2 + 2 * h];
             v1 += b[4 * t2 + 2 * h + 1];
           }
-          if constexpr (GELU) {
+          if constexpr (GELU && !RES) {
             v0 = gelu_tanh_dev(v0);
             v1 = gelu_tanh_dev(v1);
           }
@@ -984,6 +1119,7 @@ gemm_pipe_kernel(
 
     // The next tile's parameters are copied at the start of stage 1 (below),
     // so the first stage issues copies and stores only.
+    // (gated W4A8: the 8 tiles leave in slots 2, 4, .. 16, so 3 of them in or after slot 12)
     constexpr int D_SLACK1 = EPI_STORES;  // a wait that every op of the first stage may outlast
     // The stage after the next may leave outstanding the ops of the first
     // stage issued after its last copy, and those of stage 1 (its parameter
@@ -997,9 +1133,10 @@ gemm_pipe_kernel(
     // (W4A8 static FP8 output: tile pairs complete at slots 4 + j and 12 + j
     // and are stored one slot later, so 4 pairs after slot 12.)
     constexpr int D_SLACK2 = MODE == 0 ? EPI_PARAM_OPS  // stage 1 (D = 3): parameters + a stage of copies
+                             : GATED   ? 2 * 3
                              : QOUT    ? 2 * 4          // D = 2: stage 0's late stores only
                                        : 2 * (17 - kLastCopySlot);
-    static_assert(MODE == 0 || !QOUT || kLastCopySlot == 12, "W4A8 static-FP8 store schedule");
+    static_assert(MODE == 0 || !(QOUT || GATED) || kLastCopySlot == 12, "W4A8 static-FP8 and gated store schedules");
 
     int slot = 0;  // ring slot of the stage being computed
     auto run_stage = [&](int tile_k, int s_in, auto first_tag, auto br_tag) {
@@ -1052,10 +1189,126 @@ gemm_pipe_kernel(
         // the cursor is in this tile (stage D): the tile it moves to next is
         // tile_k + 1
         tile_base(cp_k + 1, nx_nb, nx_mb);
+        if constexpr (RES) residual_base(nx_mb, nx_rlo, nx_rhi, nx_rsz);
         const bool ev_live = tile_k > 0;
         int ptm = 0, ptn = 0;
         if (ev_live) tile_of(first + (tile_k - 1) * stride, tiles_m, tiles_n, ptm, ptn);
-        if constexpr (MODE == 0 && QOUT) {
+        if constexpr (GATED) {
+          // The wave's column tiles are gate, up, gate, up (i = 0 .. 3). The first
+          // step runs j outer: before MFMA (0, j) or (2, j) the lane turns the gate
+          // tile into act(gate + bias) and keeps it, one slot later the up tile into
+          // the product, and the 32 x 32 tile of the hidden state goes through the
+          // staging area; its two stores of 16 rows x 64 bytes (or, when both tiles
+          // of a row group are there as MXFP4, one of 32 rows x 32 code bytes and
+          // the rows' two scale bytes) leave one slot after that.
+          constexpr int QP = 48;  // staging pitch of MXFP4 rows: 32 bytes + 16 (16-byte aligned)
+          const uint8_t* prm = ring + PARAM_OFF + ((tile_k - 1) & 1) * PARAM_BYTES;
+          const i32x4 ry = tile_out(ptm);
+          const int m_q = ptm * 256 + wm * 32 * TM;
+          const int h_q = ptn * 128 + wn * 64;  // first hidden column of the wave
+          const i32x4 rq = make_rsrc(y, (uint32_t)M * (uint32_t)NY / 2u);
+          const i32x4 rsq = make_rsrc(y_scales, (uint32_t)(NY >> 7) * (uint32_t)M * 4u);
+          float sm[MODE == 1 ? TM : 1];
+          if constexpr (MODE == 1) {
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+              sm[j] = *reinterpret_cast<const float*>(prm + P_TOK + (wm * 32 * TM + 32 * j + r) * 4);
+          }
+          float ga[16];
+          uint32_t pk[4][2];
+          uint4 rd[2];
+          uint32_t sbs = 0, sbs_done = 0;
+          auto tile_store = [&](int j, int tt) {
+            const int col = h_q + 32 * tt + (lane & 3) * 8;
+            const uint32_t bad = ev_live && col < NY ? 0u : 0x80000000u;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              const int row = wm * 32 * TM + 32 * j + 16 * st + (lane >> 2);
+              buf_store16(ry, (((uint32_t)row * (uint32_t)NY + (uint32_t)col) * 2u) | bad, rd[st]);
+            }
+          };
+          auto group_store = [&](int j) {
+            const uint32_t bad = ev_live && h_q < NY ? 0u : 0x80000000u;
+            const uint32_t pan = (uint32_t)(h_q >> 7);
+            const int row = m_q + 32 * j + (lane >> 1);
+            const uint32_t off = (pan * (uint32_t)M + (uint32_t)row) * 64u + (uint32_t)(wn * 32 + (lane & 1) * 16);
+            buf_store16(rq, row < M ? (off | bad) : 0x80000000u, rd[0]);
+            const int srow = m_q + 32 * j + r;
+            const uint32_t soff = (pan * (uint32_t)M + (uint32_t)srow) * 4u + (uint32_t)(wn * 2);
+            buf_store2(rsq, g == 0 && srow < M ? (soff | bad) : 0x80000000u, sbs_done);
+          };
+          auto beforeg = [&](int sl) __attribute__((always_inline)) {
+            const int i = sl & 3, j = sl >> 2;
+#pragma unroll
+            for (int t2 = 0; t2 < 4; ++t2) {
+              uint2 bb = make_uint2(0u, 0u);
+              if constexpr (BIAS)
+                bb = *reinterpret_cast<const uint2*>(prm + P_BIAS + (i & 1) * 256 +
+                                                     (wn * 64 + 32 * (i >> 1) + 8 * t2 + 4 * g) * 2);
+              float v[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if constexpr (WAVES == 4) v[c] = acc_read(acc[i][j][4 * t2 + c]);
+                else v[c] = acc[i][j][4 * t2 + c];
+                const uint32_t b2 = c < 2 ? bb.x : bb.y;
+                const float b = as_float(c & 1 ? b2 & 0xFFFF0000u : b2 << 16);
+                if constexpr (MODE == 1) v[c] = BIAS ? __builtin_fmaf(v[c], sm[j], b) : v[c] * sm[j];
+                else if constexpr (BIAS) v[c] += b;
+              }
+              if ((i & 1) == 0) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ga[4 * t2 + c] = GELU ? gelu_tanh_dev(v[c]) : silu_dev(v[c]);
+              } else {
+                pk[t2][0] = pack_bf16x2(ga[4 * t2] * v[0], ga[4 * t2 + 1] * v[1]);
+                pk[t2][1] = pack_bf16x2(ga[4 * t2 + 2] * v[2], ga[4 * t2 + 3] * v[3]);
+              }
+            }
+            if constexpr (QOUT) {
+              if (i & 1) {
+                const uint32_t sb = tile_block_scale(pk, g);
+                const uint2 w = tile_codes(pk, sb);
+                *reinterpret_cast<uint2*>(ev_region + r * QP + 16 * (i >> 1) + 8 * g) = w;
+                sbs |= sb << (8 * (i >> 1));
+              }
+            }
+          };
+          auto afterg = [&](int sl) __attribute__((always_inline)) {
+            const int i = sl & 3, j = sl >> 2;
+            between0(sl);
+            if constexpr (QOUT) {
+              if (i == 0 && j > 0) group_store(j - 1);
+              if (i == 3) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                rd[0] = *reinterpret_cast<const uint4*>(ev_region + (lane >> 1) * QP + (lane & 1) * 16);
+                // the next group's writes stay behind these reads
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                sbs_done = sbs;
+                sbs = 0;
+              }
+            } else {
+              // the tile completed in the previous slot
+              if ((i & 1) == 0 && sl > 0) tile_store((sl - 1) >> 2, ((sl - 1) & 3) >> 1);
+              if (i & 1) {
+                ev8_write(pk);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                ev8_read(rd);
+                // the next tile's writes stay behind these reads
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+              }
+            }
+          };
+          mfma_step_x(cur, cur_sc, std::integral_constant<int, 0>{}, std::true_type{}, std::true_type{},
+                      std::true_type{}, beforeg, afterg);
+          const StageScales<TM> sc1 = cur_sc;
+          mfma_step_x(nxt, sc1, std::integral_constant<int, 1>{}, std::false_type{}, std::true_type{},
+                      std::false_type{}, [](int) {}, [&](int k) {
+                        between1(k);
+                        if (k == 0) {
+                          if constexpr (QOUT) group_store(TM - 1);
+                          else tile_store(TM - 1, 1);
+                        }
+                      });
+        } else if constexpr (MODE == 0 && QOUT) {
           // MXFP4 output. The wave's 128 columns are one code panel of the
           // output (64 bytes per row, rows contiguous) and one scale dword per
           // row. The first step runs j-outer: before MFMA (i, j) the lane turns
@@ -1526,6 +1779,126 @@ gemm_pipe_kernel(
       slot = slot_next;
     };
 
+    // Residual stage Q (RES): the wave's column tiles i = Q in place,
+    //   acc = residual + gate * epi(acc (* token scale) + bias),
+    // the residual from the stage's slot, in the accumulators' layout: the lane's
+    // 4 columns 8 t + 4 g .. of row group j's row r are 8 bytes of that row's
+    // chunk t. Gate values come through scalar loads where the wave's rows share
+    // one vector (a vector load's wait would drain the copies in flight), else
+    // per row.
+    auto run_residual_stage = [&](int tile_k, auto q_tag) {
+      constexpr int Q = decltype(q_tag)::value;
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE));
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int slot_next = slot + 1 == NB ? 0 : slot + 1;
+      const int slot_refill = slot == 0 ? NB - 1 : slot - 1;
+      const uint8_t* here = ring + slot * C::STAGE;
+      const uint8_t* next = ring + slot_next * C::STAGE;
+      const uint8_t* prm = ring + PARAM_OFF + (tile_k & 1) * PARAM_BYTES;
+      int tm = 0, tn = 0;
+      tile_of(first + tile_k * stride, tiles_m, tiles_n, tm, tn);
+      const int row0 = tm * 256 + wm * 32 * TM;          // the wave's first row
+      const int col0 = tn * 256 + wn * 128 + 32 * Q;     // and column
+      int g_first = 0, g_last = 0;
+      if (fuse.gate != nullptr && fuse.rows_per_group > 0) {
+        g_first = row0 / fuse.rows_per_group;
+        g_last = (min(row0 + 32 * TM, M) - 1) / fuse.rows_per_group;
+      }
+      const bool one_gate = g_first >= g_last;  // (rows all past M: any vector does)
+      float gt[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) gt[e] = 1.0f;
+      if (fuse.gate != nullptr && one_gate && row0 < M) {
+        const int64_t at0 = (int64_t)g_first * fuse.ld_mod + col0;
+#pragma unroll
+        for (int t2 = 0; t2 < 4; ++t2) {
+          if (col0 + 8 * t2 < N) {  // N is a multiple of 8
+            float f[8];
+            if (fuse.mod_bf16) {
+              const auto* p = (const __attribute__((address_space(4))) uint32_t*)(reinterpret_cast<uint64_t>(fuse.gate) +
+                                                                                 (uint64_t)(at0 + 8 * t2) * 2u);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                f[2 * e] = as_float(p[e] << 16);
+                f[2 * e + 1] = as_float(p[e] & 0xFFFF0000u);
+              }
+            } else {
+              const auto* p = (const __attribute__((address_space(4))) float*)(reinterpret_cast<uint64_t>(fuse.gate) +
+                                                                              (uint64_t)(at0 + 8 * t2) * 4u);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = p[e];
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) gt[4 * t2 + c] = g ? f[4 + c] : f[c];
+          }
+        }
+      }
+      // the tiles read first come from the last code step's first MFMAs; the
+      // waits of a VALU read of an MFMA result are spelled out all the same
+      // (the compiler does not see through the asm reads)
+      asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int lrow = xrow0 + 32 * j;  // row in the tile
+        float sm = 1.0f;
+        if constexpr (MODE == 1) sm = *reinterpret_cast<const float*>(prm + P_TOK + lrow * 4);
+        if (fuse.gate != nullptr && !one_gate) {
+          const int row = row0 + 32 * j + r;
+          const int64_t at0 = row < M ? (int64_t)(row / fuse.rows_per_group) * fuse.ld_mod : 0;
+#pragma unroll
+          for (int t2 = 0; t2 < 4; ++t2) {
+            const int col = col0 + 8 * t2 + 4 * g;
+            if (col < N) {
+              if (fuse.mod_bf16) {
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(fuse.gate) + at0 + col);
+                gt[4 * t2] = as_float(v.x << 16);
+                gt[4 * t2 + 1] = as_float(v.x & 0xFFFF0000u);
+                gt[4 * t2 + 2] = as_float(v.y << 16);
+                gt[4 * t2 + 3] = as_float(v.y & 0xFFFF0000u);
+              } else {
+                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(fuse.gate) + at0 + col);
+                gt[4 * t2] = v.x;
+                gt[4 * t2 + 1] = v.y;
+                gt[4 * t2 + 2] = v.z;
+                gt[4 * t2 + 3] = v.w;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int t2 = 0; t2 < 4; ++t2) {
+          const uint8_t* src = wn == 0 ? here + C::W_OFF + swz<C::W_RB>(lrow, t2) : here + C::X_OFF + swz<C::X_RB>(lrow, t2);
+          const uint2 rv = *reinterpret_cast<const uint2*>(src + 8 * g);
+          uint2 bb = make_uint2(0u, 0u);
+          if constexpr (BIAS)
+            bb = *reinterpret_cast<const uint2*>(prm + P_BIAS + (wn * 128 + 32 * Q + 8 * t2 + 4 * g) * 2);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v;
+            if constexpr (WAVES == 4) v = acc_read(acc[Q][j][4 * t2 + c]);
+            else v = acc[Q][j][4 * t2 + c];
+            const uint32_t b2 = c < 2 ? bb.x : bb.y, r2 = c < 2 ? rv.x : rv.y;
+            const float b = as_float(c & 1 ? b2 & 0xFFFF0000u : b2 << 16);
+            if constexpr (MODE == 1) v = BIAS ? __builtin_fmaf(v, sm, b) : v * sm;
+            else if constexpr (BIAS) v += b;
+            if constexpr (GELU) v = gelu_tanh_dev(v);
+            v = __builtin_fmaf(gt[4 * t2 + c], v, as_float(c & 1 ? r2 & 0xFFFF0000u : r2 << 16));
+            if constexpr (WAVES == 4) acc[Q][j][4 * t2 + c] = acc_write(v);
+            else acc[Q][j][4 * t2 + c] = v;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int q = j * C::PER_WAVE / TM; q < (j + 1) * C::PER_WAVE / TM; ++q) issue_one(q, slot_refill);
+      }
+#pragma unroll
+      for (int k = 0; k < STAGE_ITEMS; ++k) read_item(next, 0, 0, kStageOrder[OI][k], cur, cur_sc);
+      advance_cursor();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      slot = slot_next;
+    };
+
     // one more first stage after the last tile: it carries that tile's
     // epilogue (its own MFMAs work on zeros); the loop test is the only exit,
     // at the end of an iteration, so no path leaves between a first stage's
@@ -1538,6 +1911,15 @@ gemm_pipe_kernel(
         const int q_end = tile_k < count ? nq : 1;
         for (int s_in = 1; s_in < q_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
         for (int s_in = q_end; s_in < s_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::true_type{});
+      } else if constexpr (RES) {
+        const int q_end = tile_k < count ? nq : 1;
+        for (int s_in = 1; s_in < q_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
+        if (tile_k < count) {
+          run_residual_stage(tile_k, std::integral_constant<int, 0>{});
+          run_residual_stage(tile_k, std::integral_constant<int, 1>{});
+          run_residual_stage(tile_k, std::integral_constant<int, 2>{});
+          run_residual_stage(tile_k, std::integral_constant<int, 3>{});
+        }
       } else {
         for (int s_in = 1; s_in < s_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
       }
@@ -1557,12 +1939,12 @@ static int device_cu_count() {
   return cus;
 }
 
-template <int MODE, int KT, int NB, int WAVES, int QOUT = 0, bool LRB = false>
+template <int MODE, int KT, int NB, int WAVES, int QOUT = 0, bool LRB = false, int FUSE = kFuseNone>
 static hipError_t launch_pipe(const void* aq, const void* as, const void* wq, const void* ws, const void* bias,
                               int epi, void* y, int64_t M, int64_t N, int64_t K, hipStream_t s,
                               void* y_scales = nullptr, const float* out_amax = nullptr,
                               const void* lr_t = nullptr, const void* lr_l2 = nullptr, int lr_rank = 0,
-                              const float* out_mult = nullptr) {
+                              const float* out_mult = nullptr, const FuseArgs& fuse = FuseArgs{}) {
   static const int cus = device_cu_count();
   const int tiles_m = (int)((M + 255) / 256);
   const int tiles_n = (int)((N + 255) / 256);
@@ -1572,17 +1954,18 @@ static hipError_t launch_pipe(const void* aq, const void* as, const void* wq, co
   // the epilogue work it does
   auto go = [&](auto gelu_tag, auto bias_tag) {
     hipLaunchKernelGGL(
-        (gemm_pipe_kernel<MODE, KT, NB, decltype(gelu_tag)::value, decltype(bias_tag)::value, QOUT, LRB, WAVES>),
+        (gemm_pipe_kernel<MODE, KT, NB, decltype(gelu_tag)::value, decltype(bias_tag)::value, QOUT, LRB, WAVES, FUSE>),
         dim3(grid), dim3(64 * WAVES), 0, s, static_cast<const uint8_t*>(wq), static_cast<const uint8_t*>(ws),
         static_cast<const uint8_t*>(aq), as, static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y),
         static_cast<uint8_t*>(y_scales), out_amax, (int)M, (int)N, (int)K, tiles_m, tiles_n,
-        static_cast<const uint16_t*>(lr_t), static_cast<const uint16_t*>(lr_l2), lr_rank, out_mult);
+        static_cast<const uint16_t*>(lr_t), static_cast<const uint16_t*>(lr_l2), lr_rank, out_mult, fuse);
   };
+  const bool has_bias = bias != nullptr || (FUSE == kFuseGated && fuse.bias_up != nullptr);
   if (epi == 1) {
-    if (bias != nullptr) go(std::true_type{}, std::true_type{});
+    if (has_bias) go(std::true_type{}, std::true_type{});
     else go(std::true_type{}, std::false_type{});
   } else {
-    if (bias != nullptr) go(std::false_type{}, std::true_type{});
+    if (has_bias) go(std::false_type{}, std::true_type{});
     else go(std::false_type{}, std::false_type{});
   }
   return hipGetLastError();
@@ -1631,9 +2014,9 @@ static bool w4a4_eight_waves(int64_t M, int64_t N, int64_t K) {
 // direct kernel. 32-bit buffer offsets, and the out-of-range offset 2^31 that
 // must exceed every size, bound every operand below 2^31 bytes; row-major
 // outputs are addressed per tile (256 rows: any M), the MXFP4 output as a whole.
-static bool use_lds(int mode, int64_t M, int64_t N, int64_t K) {
+static bool use_lds(int mode, int64_t M, int64_t N, int64_t K, int64_t min_rows = 256) {
   const int64_t a_bytes = mode == 0 ? M * (K / 2) : M * K;
-  return K % kPipeKT[mode] == 0 && K / kPipeKT[mode] >= kPipeNB[mode] && N % 8 == 0 && M >= 256 && N >= 256 &&
+  return K % kPipeKT[mode] == 0 && K / kPipeKT[mode] >= kPipeNB[mode] && N % 8 == 0 && M >= min_rows && N >= 256 &&
          a_bytes < (int64_t(1) << 31) && N * (K / 2) < (int64_t(1) << 31) && 256 * N * 2 < (int64_t(1) << 31) &&
          M < (int64_t(1) << 31) / 4;
 }
@@ -1713,6 +2096,60 @@ hipError_t launch_gemm_lowrank(const void* a_codes, const void* a_scales, const 
                                                               (int)r);
   return launch_pipe<0, kPipeKT[0], kPipeNB[0], 4, 0, true>(a_codes, a_scales, w_codes, w_scales, bias, epilogue,
                                                              y, M, N, K, s, nullptr, nullptr, t, l2, (int)r);
+}
+
+// ---- the operators around the product (FUSE): few rows go to the split-K kernel
+constexpr int64_t kBlockMinRows = 65;
+
+bool gemm_residual_pipelined(int mode, int64_t M, int64_t N, int64_t K, const ResidualEpi& e) {
+  // gate vectors are read 8 columns at a time
+  const bool gate_ok = e.gate == nullptr || e.rows_per_group == 0 || e.ld_mod % 8 == 0;
+  return gate_ok && use_lds(mode, M, N, K, kBlockMinRows);
+}
+
+bool gemm_gated_pipelined(int mode, int64_t M, int64_t H, int64_t K, bool mxfp4_out) {
+  return use_lds(mode, M, 2 * H, K, kBlockMinRows) && (!mxfp4_out || (H % 128 == 0 && mxfp4_out_fits(M, H)));
+}
+
+hipError_t launch_gemm_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes,
+                                const void* w_scales, const void* bias, int epilogue, const ResidualEpi& e, void* y,
+                                int64_t M, int64_t N, int64_t K, hipStream_t s) {
+  if (!gemm_residual_pipelined(mode, M, N, K, e))
+    return launch_tokens_residual(mode, a_codes, a_scales, w_codes, w_scales, bias, epilogue, e, y, M, N, K, s);
+  FuseArgs f{};
+  f.residual = static_cast<const uint16_t*>(e.residual);
+  f.gate = e.gate;
+  f.ld_mod = e.ld_mod;
+  f.rows_per_group = (int)e.rows_per_group;
+  f.mod_bf16 = e.mod_bf16;
+  if (mode == 1)
+    return launch_pipe<1, kPipeKT[1], kPipeNB[1], 4, 0, false, kFuseResidual>(
+        a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);
+  return launch_pipe<0, kPipeKT[0], kPipeNB[0], 4, 0, false, kFuseResidual>(
+      a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);
+}
+
+template <int MODE, int WAVES, int QOUT>
+static hipError_t launch_pipe_gated(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
+                                    const void* bias_gate, const void* bias_up, int act, void* y, void* y_scales,
+                                    int64_t M, int64_t H, int64_t K, hipStream_t s) {
+  FuseArgs f{};
+  f.bias_up = static_cast<const uint16_t*>(bias_up);
+  return launch_pipe<MODE, kPipeKT[MODE], kPipeNB[MODE], WAVES, QOUT, false, kFuseGated>(
+      a_codes, a_scales, w_codes, w_scales, bias_gate, act, y, M, 2 * H, K, s, y_scales, nullptr, nullptr, nullptr, 0,
+      nullptr, f);
+}
+
+hipError_t launch_gemm_gated(int mode, const void* a_codes, const void* a_scales, const void* w_codes,
+                             const void* w_scales, const void* bias_gate, const void* bias_up, int act, void* y,
+                             void* y_scales, int64_t M, int64_t H, int64_t K, hipStream_t s) {
+  const bool q = y_scales != nullptr;
+  auto run = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, bias_gate, bias_up, act, y, y_scales, M, H, K, s); };
+  if (!gemm_gated_pipelined(mode, M, H, K, q))
+    return launch_tokens_gated(mode, a_codes, a_scales, w_codes, w_scales, bias_gate, bias_up, act, y, y_scales, M, H, K, s);
+  if (mode == 1) return run(launch_pipe_gated<1, 4, 0>);
+  if (w4a4_eight_waves(M, 2 * H, K)) return q ? run(launch_pipe_gated<0, 8, 1>) : run(launch_pipe_gated<0, 8, 0>);
+  return q ? run(launch_pipe_gated<0, 4, 1>) : run(launch_pipe_gated<0, 4, 0>);
 }
 
 const char* gemm_variant_name(int mode, int64_t M, int64_t N, int64_t K) {

@@ -109,6 +109,16 @@ hipError_t launch_tokens_gated(int mode, const void* a_codes, const void* a_scal
                                const void* w_scales, const void* bias_gate, const void* bias_up, int act, void* y,
                                void* y_scales, int64_t M, int64_t H, int64_t K, hipStream_t s);
 
+// Any shape: the pipelined kernel where it takes it, else the one above.
+bool gemm_residual_pipelined(int mode, int64_t M, int64_t N, int64_t K, const ResidualEpi& e);
+bool gemm_gated_pipelined(int mode, int64_t M, int64_t H, int64_t K, bool mxfp4_out);
+hipError_t launch_gemm_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes,
+                                const void* w_scales, const void* bias, int epilogue, const ResidualEpi& e, void* y,
+                                int64_t M, int64_t N, int64_t K, hipStream_t s);
+hipError_t launch_gemm_gated(int mode, const void* a_codes, const void* a_scales, const void* w_codes,
+                             const void* w_scales, const void* bias_gate, const void* bias_up, int act, void* y,
+                             void* y_scales, int64_t M, int64_t H, int64_t K, hipStream_t s);
+
 // Weight packing of a gated block's two projections, rows interleaved by 32.
 hipError_t launch_mxfp4_quant_gated(const void* w_gate, const void* w_up, int64_t H, int64_t K, int64_t ld, void* codes,
                                     void* scales, hipStream_t s);

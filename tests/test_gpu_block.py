@@ -19,7 +19,7 @@ import pytest
 import torch
 
 import mx_bit_quantized_amd as mxq
-from gpu_util import assert_codes_equal, host_u8
+from gpu_util import assert_codes_equal, host_u8, w4a4_waves
 
 pytestmark = pytest.mark.gpu
 
@@ -314,6 +314,9 @@ RESIDUAL_CASES = [
     (515, 776, 1280, True, True, torch.bfloat16, 200),
     (1030, 512, 512, False, False, torch.float32, None),
     (700, 300, 736, True, False, torch.float32, 350),
+    # more tiles than workgroups: a workgroup goes from one tile to the next
+    (4100, 4360, 512, True, False, torch.float32, 1500),
+    (4200, 4104, 640, False, False, torch.bfloat16, 3),
 ]
 
 
@@ -361,12 +364,20 @@ GATED_CASES = [
     (515, 416, 1280, True, False, mxq.GATED_GELU_TANH),
     (1030, 640, 512, False, True, mxq.GATED_SILU),
     (350, 160, 736, True, True, mxq.GATED_SILU),
+    # more tiles than workgroups: a workgroup goes from one tile to the next
+    (4100, 2176, 512, True, True, mxq.GATED_SILU),
+    (4200, 2080, 640, False, False, mxq.GATED_GELU_TANH),
 ]
 
 
-@pytest.mark.parametrize("mode", [mxq.W4A4, mxq.W4A8])
+@pytest.mark.parametrize("mode, waves", [(mxq.W4A4, 4), (mxq.W4A4, 8), (mxq.W4A8, 4)])
 @pytest.mark.parametrize("case", GATED_CASES, ids=lambda c: "x".join(map(str, c[:3])))
-def test_gemm_gated_matches_float64(case, mode):
+def test_gemm_gated_matches_float64(case, mode, waves):
+    with w4a4_waves(waves):
+        check_gated(case, mode)
+
+
+def check_gated(case, mode):
     m, h, k, has_bg, has_bu, act = case
     say("gated", case, mode, mxq.block_kernel_name(mode, m, h, k, gated=True))
     g = gen(m * 17 + h)
