@@ -357,6 +357,17 @@ __device__ __forceinline__ i32x4 make_rsrc(const void* base, uint32_t bytes) {
   return r;
 }
 
+// A resource held in scalar registers (the same in every lane already; computed
+// through a division or kept across branches, the compiler may not see that).
+__device__ __forceinline__ i32x4 scalar_rsrc(const i32x4& r) {
+  i32x4 s;
+  s.x = __builtin_amdgcn_readfirstlane(r.x);
+  s.y = __builtin_amdgcn_readfirstlane(r.y);
+  s.z = __builtin_amdgcn_readfirstlane(r.z);
+  s.w = 0x00020000;
+  return s;
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)((const MXQ_LDS uint8_t*)p));
 }
@@ -445,15 +456,6 @@ __device__ __forceinline__ float acc_read(float a) {
   float v;
   asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
   return v;
-}
-
-// One value written to an accumulator register at the point of use, for the
-// same reason. (The product's next instruction on it starts from zero, and its
-// next reader is acc_read, so no MFMA wait applies.)
-__device__ __forceinline__ float acc_write(float v) {
-  float a;
-  asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(a) : "v"(v));
-  return a;
 }
 
 // Range-checked 4-byte store (one data register: no late read).
@@ -560,9 +562,12 @@ struct FuseArgs {
 // 32 q .. (the wn = 0 half) ride in the W role of stage q and columns 128 + 32 q ..
 // (wn = 1) in the X role, 64 bytes per token row, so the copies run ahead through
 // the ring like any others and no load waits in the epilogue, where its wait
-// would also drain the copies in flight (vmcnt counts them in order). In stage q
-// each wave turns its column tiles i = q into the final fp32 values in place; the
-// ordinary epilogue then only rounds and stores.
+// would also drain the copies in flight (vmcnt counts them in order). The residual
+// stages are the tile's epilogue: in stage q each wave finishes, rounds and stores
+// its column tiles i = q, and the next tile's first stage carries none. (With the
+// sums finished in place and left to the ordinary epilogue, the accumulators went
+// through the vector unit twice: W4A4 32760 x 5120 x 5120 took 513 us against
+// mxq_gemm's 415.)
 template <int MODE, int KT, int NB, bool GELU, bool BIAS, int QOUT, bool LRB, int WAVES, int FUSE>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES / 4))) void
 gemm_pipe_kernel(
@@ -576,7 +581,6 @@ gemm_pipe_kernel(
   constexpr int TM = C::TM, NT = C::NT;
   static_assert(!LRB || (MODE == 0 && KT == 128 && WAVES == 4), "the branch stages take the shape of a W4A4 code stage");
   static_assert(FUSE == kFuseNone || (QOUT < 2 && !LRB && (QOUT == 0 || (MODE == 0 && FUSE == kFuseGated))), "fused forms");
-  static_assert(FUSE != kFuseResidual || WAVES == 4, "residual stages: one wave per SIMD");
   constexpr bool GATED = FUSE == kFuseGated, RES = FUSE == kFuseResidual;
   static_assert(QOUT < 2 || (MODE == 0 && WAVES == 4 && !LRB), "transformed output: W4A4, four waves");
   // ring of NB stage slots, then two tile-parameter blocks: bias slice (512
@@ -720,19 +724,6 @@ gemm_pipe_kernel(
   uint32_t cp_nb, cp_mb, nx_nb, nx_mb;  // the cursor's tile and the tile after it
   tile_base(0, cp_nb, cp_mb);
   tile_base(1, nx_nb, nx_mb);
-  // residual rows of a tile (RES): address and bytes from its first row on, so
-  // that offsets stay below 2^31 for residuals of any size
-  uint32_t cp_rlo = 0, cp_rhi = 0, cp_rsz = 0, nx_rlo = 0, nx_rhi = 0, nx_rsz = 0;
-  auto residual_base = [&](uint32_t mb, uint32_t& lo, uint32_t& hi, uint32_t& size) {
-    const uint64_t a = reinterpret_cast<uint64_t>(fuse.residual) + (uint64_t)mb * (uint64_t)N * 2u;
-    lo = (uint32_t)a;
-    hi = (uint32_t)(a >> 32);
-    size = (uint32_t)min(256, M - (int)mb) * (uint32_t)N * 2u;
-  };
-  if constexpr (RES) {
-    residual_base(cp_mb, cp_rlo, cp_rhi, cp_rsz);
-    residual_base(nx_mb, nx_rlo, nx_rhi, nx_rsz);
-  }
   // Copy q (0 .. PER_WAVE-1) of the cursor's stage into ring slot `slot`.
   // Past the last tile the copies are still issued (so the wait counts stay
   // constant and the issue has no branch) but with 2^31 added to the offset,
@@ -745,17 +736,13 @@ gemm_pipe_kernel(
     constexpr uint32_t oob = 0x80000000u;
     const uint32_t base = lds_ring + (uint32_t)slot * C::STAGE;
     // a branch stage (LRB): its rank panel, and its source rows 2 r bytes apart
-    const bool br = (LRB || RES) && cp_s >= nq;
+    const bool br = LRB && cp_s >= nq;
     const uint32_t lr_off = LRB ? (uint32_t)(cp_s - nq) * 64u : 0u;
     if (q < C::W_INSTR) {
       const uint32_t so = live ? cp_nb * (uint32_t)C::W_RB + (uint32_t)cp_s * w_panel : oob;
       if constexpr (LRB) {
         const uint32_t sl = live ? cp_nb * lr_pitch + lr_off : oob;
         lds_dma16(br ? rl2 : rw, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, br ? vwl[q] + sl : vw[q] + so);
-      } else if constexpr (RES) {
-        const uint32_t sl = live ? cp_nb * 2u + (uint32_t)(cp_s - nq) * 64u : oob;
-        const i32x4 rr = {(int)cp_rlo, (int)cp_rhi, (int)cp_rsz, 0x00020000};
-        lds_dma16(br ? rr : rw, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, br ? vwr[q] + sl : vw[q] + so);
       } else {
         lds_dma16(rw, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, vw[q] + so);
       }
@@ -766,13 +753,6 @@ gemm_pipe_kernel(
       if constexpr (LRB) {
         const uint32_t sl = live ? cp_mb * lr_pitch + lr_off : oob;
         lds_dma16(br ? rlt : rx, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, br ? vxl[qx] + sl : vx[qx] + so);
-      } else if constexpr (RES) {
-        // (an offset past the end from either part keeps the top bit: their sum
-        // is formed with or, the parts being below 2^31 otherwise)
-        const uint32_t sl = live ? cp_nb * 2u + (uint32_t)(cp_s - nq) * 64u : oob;
-        const uint32_t vr = (vxr[qx] | sl) & 0x80000000u ? 0x80000000u : vxr[qx] + sl;
-        const i32x4 rr = {(int)cp_rlo, (int)cp_rhi, (int)cp_rsz, 0x00020000};
-        lds_dma16(br ? rr : rx, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, br ? vr : vx[qx] + so);
       } else {
         lds_dma16(rx, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, vx[qx] + so);
       }
@@ -780,7 +760,7 @@ gemm_pipe_kernel(
       // the offset is below 2^31, so or-ing in the top bit puts it out of range
       // (a select of the computed offset here compiles to a branch)
       const uint32_t row0 = (cp_nb & sc_w) | (cp_mb & ~sc_w);
-      const uint32_t so = (row0 * 4u + (uint32_t)cp_s * sc_group) | (live && !br ? 0u : oob);
+      const uint32_t so = (row0 * 4u + (uint32_t)cp_s * sc_group) | (live ? 0u : oob);
       lds_dma4(rsc, base + sc_lds, vs + so);
     } else if (q == C::W_INSTR + C::X_INSTR) {
       const uint32_t so = live && !br ? cp_nb * 4u + (uint32_t)(cp_s * KT / 128) * ws_group : oob;
@@ -788,6 +768,24 @@ gemm_pipe_kernel(
     } else {
       const uint32_t so = live && !br ? cp_mb * 4u + (uint32_t)(cp_s * KT / 128) * xs_group : oob;
       lds_dma4(rxs, base + C::XS_OFF + wave * 256, vs + so);
+    }
+  };
+  // Copy q of residual stage rq of the cursor's tile (RES) into ring slot `slot`:
+  // rr the tile's residual rows, rg the tile's slice of its gate vector, which
+  // takes the place of the W scales (256 fp32 or, in half the bytes, bf16; no
+  // gate reads as zeros). The X scales' place stays unused.
+  auto issue_residual = [&](int q, int slot, int rq, const i32x4& rr, const i32x4& rg) {
+    const uint32_t base = lds_ring + (uint32_t)slot * C::STAGE;
+    const uint32_t so = cp_nb * 2u + (uint32_t)rq * 64u;
+    if (q < C::W_INSTR) {
+      lds_dma16(rr, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, vwr[q] + so);
+    } else if (q < C::W_INSTR + C::X_INSTR) {
+      const int qx = q - C::W_INSTR;
+      lds_dma16(rr, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, vxr[qx] + so);
+    } else if (q == C::W_INSTR + C::X_INSTR && wave < 4) {
+      lds_dma4(rg, base + C::WS_OFF + wave * 256, (uint32_t)(wave * 256 + lane * 4));
+    } else {
+      lds_dma4(rxs, base + C::XS_OFF + (wave & 3) * 256, 0x80000000u);
     }
   };
   auto advance_cursor = [&] {
@@ -799,11 +797,6 @@ gemm_pipe_kernel(
     const uint32_t take = 0u - (uint32_t)wrap;
     cp_nb = (nx_nb & take) | (cp_nb & ~take);
     cp_mb = (nx_mb & take) | (cp_mb & ~take);
-    if constexpr (RES) {
-      cp_rlo = (nx_rlo & take) | (cp_rlo & ~take);
-      cp_rhi = (nx_rhi & take) | (cp_rhi & ~take);
-      cp_rsz = (nx_rsz & take) | (cp_rsz & ~take);
-    }
   };
   // Tile parameters of tile k into parameter block k & 1 (issued in stage 1
   // of tile k - 1, read in the first stage of tile k + 1): the bias slice
@@ -986,7 +979,9 @@ gemm_pipe_kernel(
   // M and columns past N get an offset the range check drops.
   // (gated: two stores per 32 x 32 tile of the hidden state, or one code and one
   // scale store per 32 rows)
-  constexpr int EPI_STORES = GATED ? (QOUT ? 2 * TM : 4 * TM) : MODE == 0 ? (QOUT ? 3 * TM : WAVES == 4 ? 32 : 2 * NT) : (QOUT ? 17 : 32);
+  // (residual: none in the first stage; R_LATE per residual stage, after its copies)
+  constexpr int R_LATE = 2 * TM;
+  constexpr int EPI_STORES = RES ? 0 : GATED ? (QOUT ? 2 * TM : 4 * TM) : MODE == 0 ? (QOUT ? 3 * TM : WAVES == 4 ? 32 : 2 * NT) : (QOUT ? 17 : 32);
   constexpr int EPI_OPS = EPI_STORES + EPI_PARAM_OPS;
   // Output resource of one tile's rows for the row-major outputs (bf16, or
   // static FP8 codes): its base is the tile's first row, so the offsets stay
@@ -1069,16 +1064,14 @@ gemm_pipe_kernel(
             v0 = acc[i][j][4 * t2 + 2 * h];
             v1 = acc[i][j][4 * t2 + 2 * h + 1];
           }
-          if constexpr (RES) {
-            // final values already (the residual stages)
-          } else if constexpr (MODE == 1) {
+          if constexpr (MODE == 1) {
             v0 = BIAS ? __builtin_fmaf(v0, sm, b[4 * t2 + 2 * h]) : v0 * sm;
             v1 = BIAS ? __builtin_fmaf(v1, sm, b[4 * t2 + 2 * h + 1]) : v1 * sm;
           } else if constexpr (BIAS) {
             v0 += b[4 * t2 + 2 * h];
             v1 += b[4 * t2 + 2 * h + 1];
           }
-          if constexpr (GELU && !RES) {
+          if constexpr (GELU) {
             v0 = gelu_tanh_dev(v0);
             v1 = gelu_tanh_dev(v1);
           }
@@ -1120,7 +1113,9 @@ gemm_pipe_kernel(
     // The next tile's parameters are copied at the start of stage 1 (below),
     // so the first stage issues copies and stores only.
     // (gated W4A8: the 8 tiles leave in slots 2, 4, .. 16, so 3 of them in or after slot 12)
-    constexpr int D_SLACK1 = EPI_STORES;  // a wait that every op of the first stage may outlast
+    // (residual: the stores of the last residual stage, issued after its copies; the
+    // first tile has none before it)
+    constexpr int D_SLACK1 = RES ? R_LATE : EPI_STORES;  // a wait that every op of the first stage may outlast
     // The stage after the next may leave outstanding the ops of the first
     // stage issued after its last copy, and those of stage 1 (its parameter
     // copies come before its stage copies): W4A4 issues every epilogue store
@@ -1133,20 +1128,30 @@ gemm_pipe_kernel(
     // (W4A8 static FP8 output: tile pairs complete at slots 4 + j and 12 + j
     // and are stored one slot later, so 4 pairs after slot 12.)
     constexpr int D_SLACK2 = MODE == 0 ? EPI_PARAM_OPS  // stage 1 (D = 3): parameters + a stage of copies
+                             : RES     ? 0
                              : GATED   ? 2 * 3
                              : QOUT    ? 2 * 4          // D = 2: stage 0's late stores only
                                        : 2 * (17 - kLastCopySlot);
     static_assert(MODE == 0 || !(QOUT || GATED) || kLastCopySlot == 12, "W4A8 static-FP8 and gated store schedules");
 
+    // A stage opening in or after the residual stages may leave outstanding, beside
+    // the copies it does not need, the stores issued since the last copy that it
+    // does: those of the stage before (one residual stage), and with copies three
+    // stages ahead those of the stage before that one too (two).
+    constexpr int R_WAIT1 = R_LATE, R_WAIT2 = D >= 3 ? 2 * R_LATE : R_LATE;
+    static_assert(!RES || WAIT_BASE + R_WAIT2 <= 63, "vmcnt range");
     int slot = 0;  // ring slot of the stage being computed
-    auto run_stage = [&](int tile_k, int s_in, auto first_tag, auto br_tag) {
+    // `copy(q, slot)` issues the stage's copies (those of the stage D ahead)
+    auto run_stage_x = [&](int tile_k, int s_in, auto first_tag, auto br_tag, auto&& copy) {
       constexpr bool FIRST = decltype(first_tag)::value;
       constexpr bool BR = decltype(br_tag)::value;
       if (tile_k > 0 || s_in > 0) {
         // the stage after the first one may leave all of the first stage's
         // operations outstanding; the one after that, those issued after its
         // last copy
-        if (s_in >= 1 && s_in <= D - 2) __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE + D_SLACK1));
+        if (RES && tile_k == 0 && s_in <= D - 2) __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE));
+        else if (RES && s_in == 0) __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE + R_WAIT2));
+        else if (s_in >= 1 && s_in <= D - 2) __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE + D_SLACK1));
         else if (s_in == D - 1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE + D_SLACK2));
         else __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE));
         __builtin_amdgcn_s_barrier();
@@ -1169,14 +1174,14 @@ gemm_pipe_kernel(
       StageScales<TM> nxt_sc;
       auto between0 = [&](int k) {
         if (k < DATA_ITEMS) read_item(here, 1, 0, kStepOrder[OI][k], nxt, nxt_sc);
-        if (kCopyAt[k] >= 0) issue_one(kCopyAt[k], slot_refill);
+        if (kCopyAt[k] >= 0) copy(kCopyAt[k], slot_refill);
       };
       // the next stage's STAGE_ITEMS reads spread over the NT slots of step 1
       auto between1 = [&](int k) {
 #pragma unroll
         for (int it = k * STAGE_ITEMS / NT; it < (k + 1) * STAGE_ITEMS / NT; ++it)
           read_item(next, 0, next_half, kStageOrder[OI][it], cur, cur_sc);
-        if (kCopyAt[NT + k] >= 0) issue_one(kCopyAt[NT + k], slot_refill);
+        if (kCopyAt[NT + k] >= 0) copy(kCopyAt[NT + k], slot_refill);
       };
       if constexpr (!FIRST && BR) {
         mfma_step_bf(cur, between0);
@@ -1189,7 +1194,7 @@ gemm_pipe_kernel(
         // the cursor is in this tile (stage D): the tile it moves to next is
         // tile_k + 1
         tile_base(cp_k + 1, nx_nb, nx_mb);
-        if constexpr (RES) residual_base(nx_mb, nx_rlo, nx_rhi, nx_rsz);
+        if constexpr (!RES) {
         const bool ev_live = tile_k > 0;
         int ptm = 0, ptn = 0;
         if (ev_live) tile_of(first + (tile_k - 1) * stride, tiles_m, tiles_n, ptm, ptn);
@@ -1773,22 +1778,38 @@ gemm_pipe_kernel(
                         if (k == 0) unit_store(3, 1);
                       });
         }
+        } else {
+          // the sums start from zero; the tile before has left already
+          mfma_step_x(cur, cur_sc, std::integral_constant<int, 0>{}, std::true_type{}, std::false_type{},
+                      std::false_type{}, [](int) {}, between0);
+          const StageScales<TM> sc1 = cur_sc;
+          mfma_step(nxt, sc1, std::integral_constant<int, 1>{}, between1);
+        }
       }
       advance_cursor();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       slot = slot_next;
     };
 
-    // Residual stage Q (RES): the wave's column tiles i = Q in place,
-    //   acc = residual + gate * epi(acc (* token scale) + bias),
+    auto run_stage = [&](int tile_k, int s_in, auto first_tag, auto br_tag) {
+      run_stage_x(tile_k, s_in, first_tag, br_tag, issue_one);
+    };
+
+    // Residual stage Q (RES): for the wave's column tiles i = Q
+    //   y = residual + gate * epi(acc (* token scale) + bias),
     // the residual from the stage's slot, in the accumulators' layout: the lane's
     // 4 columns 8 t + 4 g .. of row group j's row r are 8 bytes of that row's
-    // chunk t. Gate values come through scalar loads where the wave's rows share
-    // one vector (a vector load's wait would drain the copies in flight), else
-    // per row.
-    auto run_residual_stage = [&](int tile_k, auto q_tag) {
+    // chunk t. All LDS reads, those of the next stage's first fragments too, are
+    // issued before the arithmetic (one wave per SIMD has nothing else to cover
+    // their latency with), the copies in the first half, and row group j's tile
+    // leaves through the staging area while group j + 1 is computed: 2 stores of
+    // 16 rows x 64 bytes, all of them after the stage's last copy. ROWS: a gate
+    // vector per row (a tile with rows of several groups), from memory; else the
+    // tile's one vector from the slot, or none.
+    auto run_residual_stage = [&](int tile_k, auto q_tag, auto rows_tag, int row_t, int col_t, const i32x4& ry, auto&& copy) {
       constexpr int Q = decltype(q_tag)::value;
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE));
+      constexpr bool ROWS = decltype(rows_tag)::value;
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE + (Q == 0 ? 0 : Q == 1 ? R_WAIT1 : R_WAIT2)));
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const int slot_next = slot + 1 == NB ? 0 : slot + 1;
@@ -1796,104 +1817,118 @@ gemm_pipe_kernel(
       const uint8_t* here = ring + slot * C::STAGE;
       const uint8_t* next = ring + slot_next * C::STAGE;
       const uint8_t* prm = ring + PARAM_OFF + (tile_k & 1) * PARAM_BYTES;
-      int tm = 0, tn = 0;
-      tile_of(first + tile_k * stride, tiles_m, tiles_n, tm, tn);
-      const int row0 = tm * 256 + wm * 32 * TM;          // the wave's first row
-      const int col0 = tn * 256 + wn * 128 + 32 * Q;     // and column
-      int g_first = 0, g_last = 0;
-      if (fuse.gate != nullptr && fuse.rows_per_group > 0) {
-        g_first = row0 / fuse.rows_per_group;
-        g_last = (min(row0 + 32 * TM, M) - 1) / fuse.rows_per_group;
-      }
-      const bool one_gate = g_first >= g_last;  // (rows all past M: any vector does)
-      float gt[16];
+      const int wcol = wn * 128 + 32 * Q;  // the wave's first column in the tile, and per lane + 8 t + 4 g
+      uint2 rv[TM][4];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) gt[e] = 1.0f;
-      if (fuse.gate != nullptr && one_gate && row0 < M) {
-        const int64_t at0 = (int64_t)g_first * fuse.ld_mod + col0;
+      for (int j = 0; j < TM; ++j)
 #pragma unroll
         for (int t2 = 0; t2 < 4; ++t2) {
-          if (col0 + 8 * t2 < N) {  // N is a multiple of 8
-            float f[8];
-            if (fuse.mod_bf16) {
-              const auto* p = (const __attribute__((address_space(4))) uint32_t*)(reinterpret_cast<uint64_t>(fuse.gate) +
-                                                                                 (uint64_t)(at0 + 8 * t2) * 2u);
+          const int lrow = xrow0 + 32 * j;
+          const uint32_t off = wn == 0 ? C::W_OFF + swz<C::W_RB>(lrow, t2) : C::X_OFF + swz<C::X_RB>(lrow, t2);
+          rv[j][t2] = *reinterpret_cast<const uint2*>(here + off + 8 * g);
+        }
+      const bool gated = !ROWS && fuse.gate != nullptr;
+      float gt[16], bs[16], sm[TM];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                f[2 * e] = as_float(p[e] << 16);
-                f[2 * e + 1] = as_float(p[e] & 0xFFFF0000u);
-              }
-            } else {
-              const auto* p = (const __attribute__((address_space(4))) float*)(reinterpret_cast<uint64_t>(fuse.gate) +
-                                                                              (uint64_t)(at0 + 8 * t2) * 4u);
+      for (int t2 = 0; t2 < 4; ++t2) {
+        if constexpr (BIAS) {
+          const uint2 v = *reinterpret_cast<const uint2*>(prm + P_BIAS + (wcol + 8 * t2 + 4 * g) * 2);
+          bs[4 * t2] = as_float(v.x << 16);
+          bs[4 * t2 + 1] = as_float(v.x & 0xFFFF0000u);
+          bs[4 * t2 + 2] = as_float(v.y << 16);
+          bs[4 * t2 + 3] = as_float(v.y & 0xFFFF0000u);
+        }
+        if constexpr (!ROWS) {
+          // both widths are read (a choice of loads would be a branch), then chosen
+          const uint2 h = *reinterpret_cast<const uint2*>(here + C::WS_OFF + (wcol + 8 * t2 + 4 * g) * 2);
+          const float4 f = *reinterpret_cast<const float4*>(here + C::WS_OFF + (wcol + 8 * t2 + 4 * g) * 4);
+          const float hb[4] = {as_float(h.x << 16), as_float(h.x & 0xFFFF0000u), as_float(h.y << 16),
+                               as_float(h.y & 0xFFFF0000u)};
+          const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = p[e];
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) gt[4 * t2 + c] = g ? f[4 + c] : f[c];
-          }
+          for (int c = 0; c < 4; ++c) gt[4 * t2 + c] = gated ? (fuse.mod_bf16 ? hb[c] : ff[c]) : 1.0f;
         }
       }
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        sm[j] = 1.0f;
+        if constexpr (MODE == 1) sm[j] = *reinterpret_cast<const float*>(prm + P_TOK + (xrow0 + 32 * j) * 4);
+      }
+#pragma unroll
+      for (int k = 0; k < STAGE_ITEMS; ++k) read_item(next, 0, 0, kStageOrder[OI][k], cur, cur_sc);
       // the tiles read first come from the last code step's first MFMAs; the
       // waits of a VALU read of an MFMA result are spelled out all the same
       // (the compiler does not see through the asm reads)
       asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      uint4 rd[2];
+      auto tile_store = [&](int j) {
+        const int col = col_t + wcol + (lane & 3) * 8;
+        const uint32_t bad = col < N ? 0u : 0x80000000u;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const int row = wm * 32 * TM + 32 * j + 16 * st + (lane >> 2);
+          buf_store16(ry, (((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u) | bad, rd[st]);
+        }
+      };
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
-        const int lrow = xrow0 + 32 * j;  // row in the tile
-        float sm = 1.0f;
-        if constexpr (MODE == 1) sm = *reinterpret_cast<const float*>(prm + P_TOK + lrow * 4);
-        if (fuse.gate != nullptr && !one_gate) {
-          const int row = row0 + 32 * j + r;
+        if constexpr (ROWS) {
+          const int row = row_t + xrow0 + 32 * j;
           const int64_t at0 = row < M ? (int64_t)(row / fuse.rows_per_group) * fuse.ld_mod : 0;
 #pragma unroll
           for (int t2 = 0; t2 < 4; ++t2) {
-            const int col = col0 + 8 * t2 + 4 * g;
-            if (col < N) {
-              if (fuse.mod_bf16) {
-                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(fuse.gate) + at0 + col);
-                gt[4 * t2] = as_float(v.x << 16);
-                gt[4 * t2 + 1] = as_float(v.x & 0xFFFF0000u);
-                gt[4 * t2 + 2] = as_float(v.y << 16);
-                gt[4 * t2 + 3] = as_float(v.y & 0xFFFF0000u);
-              } else {
-                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(fuse.gate) + at0 + col);
-                gt[4 * t2] = v.x;
-                gt[4 * t2 + 1] = v.y;
-                gt[4 * t2 + 2] = v.z;
-                gt[4 * t2 + 3] = v.w;
-              }
+            const int col = min(col_t + wcol + 8 * t2 + 4 * g, N - 4);  // (columns past N are not stored)
+            if (fuse.mod_bf16) {
+              const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(fuse.gate) + at0 + col);
+              gt[4 * t2] = as_float(v.x << 16);
+              gt[4 * t2 + 1] = as_float(v.x & 0xFFFF0000u);
+              gt[4 * t2 + 2] = as_float(v.y << 16);
+              gt[4 * t2 + 3] = as_float(v.y & 0xFFFF0000u);
+            } else {
+              const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(fuse.gate) + at0 + col);
+              gt[4 * t2] = v.x;
+              gt[4 * t2 + 1] = v.y;
+              gt[4 * t2 + 2] = v.z;
+              gt[4 * t2 + 3] = v.w;
             }
           }
         }
+        uint32_t pk[4][2];
 #pragma unroll
         for (int t2 = 0; t2 < 4; ++t2) {
-          const uint8_t* src = wn == 0 ? here + C::W_OFF + swz<C::W_RB>(lrow, t2) : here + C::X_OFF + swz<C::X_RB>(lrow, t2);
-          const uint2 rv = *reinterpret_cast<const uint2*>(src + 8 * g);
-          uint2 bb = make_uint2(0u, 0u);
-          if constexpr (BIAS)
-            bb = *reinterpret_cast<const uint2*>(prm + P_BIAS + (wn * 128 + 32 * Q + 8 * t2 + 4 * g) * 2);
+          float o[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float v;
             if constexpr (WAVES == 4) v = acc_read(acc[Q][j][4 * t2 + c]);
             else v = acc[Q][j][4 * t2 + c];
-            const uint32_t b2 = c < 2 ? bb.x : bb.y, r2 = c < 2 ? rv.x : rv.y;
-            const float b = as_float(c & 1 ? b2 & 0xFFFF0000u : b2 << 16);
-            if constexpr (MODE == 1) v = BIAS ? __builtin_fmaf(v, sm, b) : v * sm;
-            else if constexpr (BIAS) v += b;
+            const uint32_t r2 = c < 2 ? rv[j][t2].x : rv[j][t2].y;
+            if constexpr (MODE == 1) v = BIAS ? __builtin_fmaf(v, sm[j], bs[4 * t2 + c]) : v * sm[j];
+            else if constexpr (BIAS) v += bs[4 * t2 + c];
             if constexpr (GELU) v = gelu_tanh_dev(v);
-            v = __builtin_fmaf(gt[4 * t2 + c], v, as_float(c & 1 ? r2 & 0xFFFF0000u : r2 << 16));
-            if constexpr (WAVES == 4) acc[Q][j][4 * t2 + c] = acc_write(v);
-            else acc[Q][j][4 * t2 + c] = v;
+            o[c] = __builtin_fmaf(gt[4 * t2 + c], v, as_float(c & 1 ? r2 & 0xFFFF0000u : r2 << 16));
+          }
+          pk[t2][0] = pack_bf16x2(o[0], o[1]);
+          pk[t2][1] = pack_bf16x2(o[2], o[3]);
+          constexpr int STEPS = 2 * TM;  // the copies go out in the first half
+          if (j < TM / 2) {
+#pragma unroll
+            for (int q = (4 * j + t2) * C::PER_WAVE / STEPS; q < (4 * j + t2 + 1) * C::PER_WAVE / STEPS; ++q)
+              copy(q, slot_refill);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int q = j * C::PER_WAVE / TM; q < (j + 1) * C::PER_WAVE / TM; ++q) issue_one(q, slot_refill);
+        // (with two row groups the last copies follow the first group's arithmetic,
+        // so its tile, too, leaves after them)
+        if (j > 0) tile_store(j - 1);
+        ev8_write(pk);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        ev8_read(rd);
+        // the next tile's writes stay behind these reads
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
-#pragma unroll
-      for (int k = 0; k < STAGE_ITEMS; ++k) read_item(next, 0, 0, kStageOrder[OI][k], cur, cur_sc);
+      tile_store(TM - 1);
       advance_cursor();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       slot = slot_next;
@@ -1903,7 +1938,9 @@ gemm_pipe_kernel(
     // epilogue (its own MFMAs work on zeros); the loop test is the only exit,
     // at the end of an iteration, so no path leaves between a first stage's
     // MFMAs and the stages that use their sums
-    for (int tile_k = 0; tile_k <= count; ++tile_k) {
+    // (residual stages leave nothing for it: the loop ends with the last tile)
+    const int tile_end = RES ? count : count + 1;
+    for (int tile_k = 0; tile_k < tile_end; ++tile_k) {
       run_stage(tile_k, 0, std::true_type{}, std::false_type{});
       const int s_end = tile_k < count ? n_stages : 1;
       if constexpr (LRB) {
@@ -1912,13 +1949,48 @@ gemm_pipe_kernel(
         for (int s_in = 1; s_in < q_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
         for (int s_in = q_end; s_in < s_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::true_type{});
       } else if constexpr (RES) {
-        const int q_end = tile_k < count ? nq : 1;
-        for (int s_in = 1; s_in < q_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
+        // The copies issued D stages ahead change kind with the stage they are
+        // for, so the loop is cut there (a choice per copy would cost every code
+        // stage): code stages nq - D .. nq - 1 copy residual stages 0 .. D - 1 of
+        // their own tile, residual stage Q copies residual stage Q + D or, past the
+        // last, the next tile's first code stages.
         if (tile_k < count) {
-          run_residual_stage(tile_k, std::integral_constant<int, 0>{});
-          run_residual_stage(tile_k, std::integral_constant<int, 1>{});
-          run_residual_stage(tile_k, std::integral_constant<int, 2>{});
-          run_residual_stage(tile_k, std::integral_constant<int, 3>{});
+          for (int s_in = 1; s_in < nq - D; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
+          int ctm = 0, ctn = 0;
+          tile_of(first + tile_k * stride, tiles_m, tiles_n, ctm, ctn);
+          const int row_t = ctm * 256, col_t = ctn * 256;
+          const int rows = min(256, M - row_t);
+          const i32x4 ry = scalar_rsrc(tile_out(ctm));
+          const i32x4 rr =
+              scalar_rsrc(make_rsrc(fuse.residual + (size_t)row_t * (size_t)N, (uint32_t)rows * (uint32_t)N * 2u));
+          int group = 0, gate_kind = fuse.gate != nullptr ? 1 : 0;
+          if (gate_kind != 0 && fuse.rows_per_group > 0) {
+            group = row_t / fuse.rows_per_group;
+            if ((row_t + rows - 1) / fuse.rows_per_group != group) gate_kind = 2;
+          }
+          const uint32_t g_elt = fuse.mod_bf16 ? 2u : 4u;
+          const i32x4 rg = scalar_rsrc(make_rsrc(static_cast<const uint8_t*>(fuse.gate) +
+                                                     ((size_t)group * (size_t)fuse.ld_mod + (size_t)col_t) * g_elt,
+                                                 gate_kind == 1 ? (uint32_t)(N - col_t) * g_elt : 0u));
+          for (int s_in = nq - D > 1 ? nq - D : 1; s_in < nq; ++s_in)
+            run_stage_x(tile_k, s_in, std::false_type{}, std::false_type{},
+                        [&](int q, int sl) { issue_residual(q, sl, cp_s - nq, rr, rg); });
+          auto residual_stage = [&](auto q_tag, auto rows_tag) {
+            constexpr int Q = decltype(q_tag)::value;
+            if constexpr (Q + D < 4)
+              run_residual_stage(tile_k, q_tag, rows_tag, row_t, col_t, ry,
+                                 [&](int q, int sl) { issue_residual(q, sl, Q + D, rr, rg); });
+            else
+              run_residual_stage(tile_k, q_tag, rows_tag, row_t, col_t, ry, issue_one);
+          };
+          auto residual_stages = [&](auto rows_tag) {
+            residual_stage(std::integral_constant<int, 0>{}, rows_tag);
+            residual_stage(std::integral_constant<int, 1>{}, rows_tag);
+            residual_stage(std::integral_constant<int, 2>{}, rows_tag);
+            residual_stage(std::integral_constant<int, 3>{}, rows_tag);
+          };
+          if (gate_kind == 2) residual_stages(std::true_type{});
+          else residual_stages(std::false_type{});
         }
       } else {
         for (int s_in = 1; s_in < s_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
@@ -2124,6 +2196,9 @@ hipError_t launch_gemm_residual(int mode, const void* a_codes, const void* a_sca
   f.mod_bf16 = e.mod_bf16;
   if (mode == 1)
     return launch_pipe<1, kPipeKT[1], kPipeNB[1], 4, 0, false, kFuseResidual>(
+        a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);
+  if (w4a4_eight_waves(M, N, K))
+    return launch_pipe<0, kPipeKT[0], kPipeNB[0], 8, 0, false, kFuseResidual>(
         a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);
   return launch_pipe<0, kPipeKT[0], kPipeNB[0], 4, 0, false, kFuseResidual>(
       a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);

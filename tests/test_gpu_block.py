@@ -317,12 +317,18 @@ RESIDUAL_CASES = [
     # more tiles than workgroups: a workgroup goes from one tile to the next
     (4100, 4360, 512, True, False, torch.float32, 1500),
     (4200, 4104, 640, False, False, torch.bfloat16, 3),
+    (4353, 4360, 768, True, False, None, None),
 ]
 
 
-@pytest.mark.parametrize("mode", [mxq.W4A4, mxq.W4A8])
+@pytest.mark.parametrize("mode, waves", [(mxq.W4A4, 4), (mxq.W4A4, 8), (mxq.W4A8, 4)])
 @pytest.mark.parametrize("case", RESIDUAL_CASES, ids=lambda c: "x".join(map(str, c[:3])))
-def test_gemm_residual_matches_float64(case, mode):
+def test_gemm_residual_matches_float64(case, mode, waves):
+    with w4a4_waves(waves):
+        check_residual(case, mode)
+
+
+def check_residual(case, mode):
     m, n, k, has_bias, gelu, gate_type, rpg = case
     say("residual", case, mode, mxq.block_kernel_name(mode, m, n, k))
     g = gen(m * 31 + n)
