@@ -672,5 +672,15 @@ def lowrank_up(y_pre, t, l2, epilogue=EPI_NONE, y=None, stream=None):
 
 # ------------------------------------------------- around the linears ----
 
-from .block import (GATED_GELU_TANH, GATED_SILU, NORM_LAYER, NORM_MAX_K, NORM_NONE, NORM_RMS,  # noqa: E402,F401
-                    block_kernel_name, gemm_gated, gemm_residual, norm_quantize, quantize_weight_gated_mxfp4)
+_BLOCK = ("GATED_GELU_TANH", "GATED_SILU", "NORM_LAYER", "NORM_MAX_K", "NORM_NONE", "NORM_RMS", "block_kernel_name",
+          "gemm_gated", "gemm_residual", "norm_quantize", "quantize_weight_gated_mxfp4")
+
+
+def __getattr__(name):
+    """Names of block.py, which imports torch: bound here at their first use."""
+    if name not in _BLOCK:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import block
+
+    globals().update({n: getattr(block, n) for n in _BLOCK})
+    return globals()[name]

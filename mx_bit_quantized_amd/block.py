@@ -14,7 +14,12 @@ Shapes and devices are checked here, sizes and alignment in the library; nothing
 import contextlib
 import ctypes
 
-from . import (EPI_NONE, POLICY_BF16, W4A4, W4A8, _check, _torch, lib, mx_scale_shape)
+import torch
+
+from . import EPI_NONE, POLICY_BF16, W4A8, _check, lib, mx_scale_shape
+
+# the current stream's handle by device index, without a Stream object (None where this torch has no such call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 GATED_SILU, GATED_GELU_TANH = 0, 1
@@ -50,7 +55,7 @@ _bound = None
 def _lib():
     global _bound
     handle = lib()
-    if handle is not _bound:
+    if handle is not _bound:  # (a test may load another build)
         for name, (res, args) in _SIGS.items():
             fn = getattr(handle, name)
             fn.restype = res
@@ -59,92 +64,99 @@ def _lib():
     return handle
 
 
-def _device(t, name):
-    torch = _torch()
+# The checks below run on every call of operators that may take a few microseconds on the GPU: plain comparisons,
+# device indices instead of device objects, the raw stream handle.
+
+def _index(t, name):
+    """Device index of a GPU tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    return t.device
+    return t.get_device()
 
 
-def _ptr(t, name, device, dtype, shape=None):
-    """Address of a contiguous tensor on ``device`` (None for None)."""
+def _same(t, name, dev):
+    if _index(t, name) != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{dev}")
+
+
+def _ptr(t, name, dev, dtype, shape):
+    """Address of a contiguous tensor of that device, dtype and shape (None for None)."""
     if t is None:
         return None
-    if _device(t, name) != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    _same(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (no implicit copies)")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _rows(t, name, device, shape):
+def _rows(t, name, dev, shape):
     """(address, row stride) of a bf16 matrix whose rows may be strided."""
-    torch = _torch()
-    if _device(t, name) != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    _same(t, name, dev)
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must have dtype torch.bfloat16, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if shape[0] > 1 and t.stride(0) < shape[1] or shape[1] > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    ld, unit = t.stride()
+    if shape[0] > 1 and ld < shape[1] or unit != 1:
         raise ValueError(f"{name} must have unit stride along its rows and rows that do not overlap")
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
+    return t.data_ptr(), (ld if shape[0] > 1 else shape[1])
 
 
-def _vectors(named, device, m, n, rows_per_group):
+def _vectors(named, dev, m, n, rows_per_group):
     """Modulation vectors ([n] or [groups, n], rows may be strided) -> (addresses, mod_type, ld_mod, rows_per_group)."""
-    torch = _torch()
-    ptrs, kind, ld, groups = [], None, n, 1
+    ptrs, kind = [], None
     for name, t in named:
         if t is None:
             ptrs.append(None)
             continue
-        if _device(t, name) != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        _same(t, name, dev)
         if t.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-        v = t if t.dim() == 2 else t.unsqueeze(0)
-        if v.dim() != 2 or v.shape[1] != n or (n > 1 and v.stride(1) != 1) or v.shape[0] < 1:
-            raise ValueError(f"{name} must be [{n}] or [groups, {n}] with unit stride along {n}, got {tuple(t.shape)}")
-        this = (t.dtype, v.shape[0], v.stride(0) if v.shape[0] > 1 else n)
+        shape, stride = t.shape, t.stride()
+        if not 1 <= len(shape) <= 2 or shape[-1] != n or (n > 1 and stride[-1] != 1) or shape[0] < 1:
+            raise ValueError(f"{name} must be [{n}] or [groups, {n}] with unit stride along {n}, got {tuple(shape)}")
+        groups = shape[0] if len(shape) == 2 else 1
+        this = (t.dtype, groups, stride[0] if groups > 1 else n)
         if kind is None:
             kind = this
-        elif kind[:2] != this[:2] or (kind[1] > 1 and kind[2] != this[2]):
+        elif kind != this:
             raise ValueError(f"modulation vectors must share dtype, groups and row stride: {name} has {this}, not {kind}")
-        ptrs.append(v.data_ptr())
+        ptrs.append(t.data_ptr())
     if kind is None:
         return ptrs, 0, n, 0
-    groups, ld = kind[1], kind[2]
+    dtype, groups, ld = kind
     if groups == 1 and (rows_per_group is None or rows_per_group >= m):
-        rpg = 0
+        rows_per_group = 0
     elif rows_per_group is None or rows_per_group < 1:
         raise ValueError(f"modulation vectors of {groups} groups need rows_per_group")
     elif groups * rows_per_group < m:
         raise ValueError(f"{groups} groups of {rows_per_group} rows do not cover {m} rows")
-    else:
-        rpg = int(rows_per_group)
-    return ptrs, (0 if kind[0] == torch.float32 else 1), ld, rpg
+    return ptrs, (0 if dtype == torch.float32 else 1), ld, rows_per_group
 
 
-def _on(device, stream):
-    """(stream handle, context in which to allocate and launch) for work on ``device``."""
-    torch = _torch()
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    """(stream handle, context in which to allocate and launch) for work on device ``dev``."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
         return stream.cuda_stream, torch.cuda.stream(stream)  # (sets the device too)
-    ctx = contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-    return torch.cuda.current_stream(device).cuda_stream, ctx
+    handle = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev)
+    return handle, (_HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev))
 
 
 def _matrix(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D [rows, K]")
-    return int(t.shape[0]), int(t.shape[1])
+    return t.shape
 
 
 def norm_quantize(mode, x, branch=None, gate=None, branch_scale=1.0, post_norm=NORM_NONE, post_weight=None,
@@ -158,66 +170,81 @@ def norm_quantize(mode, x, branch=None, gate=None, branch_scale=1.0, post_norm=N
     (in place); ``write_h=False`` keeps h out of memory. gate, scale and shift are [K] or [groups, K], float32 or bfloat16
     alike, row m using vector m // rows_per_group.
     """
-    torch = _torch()
-    device = _device(x, "x")
+    dev = _index(x, "x")
     m, k = _matrix(x, "x")
-    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
-    a = NormArgs()
-    a.x, a.ldx = _rows(x, "x", device, (m, k))
-    (a.gate, a.scale, a.shift), a.mod_type, a.ld_mod, a.rows_per_group = _vectors(
-        (("gate", gate), ("scale", scale), ("shift", shift)), device, m, k, rows_per_group)
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight), ("bias", bias)):
-        if t is not None:
-            setattr(a, name, _ptr(t, name, device, bf16, (k,)))
-    if act_mult is not None:
-        a.act_mult = _ptr(act_mult, "act_mult", device, f32, (k,))
-    a.M, a.K = m, k
-    a.norm, a.post_norm, a.eps, a.branch_scale = int(norm), int(post_norm), float(eps), float(branch_scale)
-    handle, ctx = _on(device, stream)
+    bf16, u8 = torch.bfloat16, torch.uint8
+    px, ldx = _rows(x, "x", dev, (m, k))
+    if gate is None and scale is None and shift is None:
+        pg = psc = psh = None
+        mod_type, ld_mod, rpg = 0, k, 0
+    else:
+        (pg, psc, psh), mod_type, ld_mod, rpg = _vectors((("gate", gate), ("scale", scale), ("shift", shift)), dev, m, k,
+                                                         rows_per_group)
+    vec = (k,)
+    ppw, ppb = _ptr(post_weight, "post_weight", dev, bf16, vec), _ptr(post_bias, "post_bias", dev, bf16, vec)
+    pw, pbias = _ptr(weight, "weight", dev, bf16, vec), _ptr(bias, "bias", dev, bf16, vec)
+    pm = _ptr(act_mult, "act_mult", dev, torch.float32, vec)
+    handle, ctx = _on(dev, stream)
     with ctx:
+        pb = ph = None
+        ldb = ldh = k
         if branch is not None:
-            a.branch, a.ldb = _rows(branch, "branch", device, (m, k))
+            pb, ldb = _rows(branch, "branch", dev, (m, k))
             if write_h:
                 if h is None:
-                    h = torch.empty((m, k), dtype=bf16, device=device)
-                a.h, a.ldh = _rows(h, "h", device, (m, k))
+                    h = torch.empty((m, k), dtype=bf16, device=x.device)
+                    ph = h.data_ptr()
+                else:
+                    ph, ldh = _rows(h, "h", dev, (m, k))
             else:
                 h = None
         elif h is None:
             h = x if write_h else None
         else:
             raise ValueError("h is an output of a call with a branch")
+        pos = None
         if mode == POLICY_BF16:
             if out is None:
-                out = torch.empty((m, k), dtype=bf16, device=device)
-            a.out = _ptr(out, "out", device, bf16, (m, k))
+                out = torch.empty((m, k), dtype=bf16, device=x.device)
+                po = out.data_ptr()
+            else:
+                po = _ptr(out, "out", dev, bf16, (m, k))
         else:
             wide = mode == W4A8
+            codes_shape = (m, k if wide else k // 2)
+            scales_shape, scales_type = ((m,), torch.float32) if wide else (mx_scale_shape(m, k), u8)
             if out is None:
-                out = torch.empty((m, k if wide else k // 2), dtype=u8, device=device)
+                out = torch.empty(codes_shape, dtype=u8, device=x.device)
+                po = out.data_ptr()
+            else:
+                po = _ptr(out, "out", dev, u8, codes_shape)
             if out_scales is None:
-                out_scales = torch.empty((m,) if wide else mx_scale_shape(m, k), dtype=f32 if wide else u8, device=device)
-            a.out = _ptr(out, "out", device, u8, (m, k if wide else k // 2))
-            a.out_scales = _ptr(out_scales, "out_scales", device, f32 if wide else u8,
-                                (m,) if wide else mx_scale_shape(m, k))
-        st = _lib().mxq_norm_quantize(int(mode), ctypes.byref(a), handle)
+                out_scales = torch.empty(scales_shape, dtype=scales_type, device=x.device)
+                pos = out_scales.data_ptr()
+            else:
+                pos = _ptr(out_scales, "out_scales", dev, scales_type, scales_shape)
+        args = NormArgs(px, pb, pg, ppw, ppb, pw, pbias, psc, psh, pm, ph, po, pos, m, k, ldx, ldb, ldh, ld_mod, rpg,
+                        post_norm, norm, mod_type, eps, branch_scale)
+        st = _lib().mxq_norm_quantize(mode, args, handle)
     _check(st, "norm_quantize")
     return out, out_scales, h
 
 
 def _operands(mode, a_codes, a_scales, w_codes, w_scales):
     """Device, (M, weight rows, K) and addresses of a product's quantized operands."""
-    torch = _torch()
-    device = _device(w_codes, "w_codes")
+    dev = _index(w_codes, "w_codes")
     n, half = _matrix(w_codes, "w_codes")
     k = 2 * half
-    m = int(a_codes.shape[0])
+    m = a_codes.shape[0]
     u8 = torch.uint8
-    ptrs = [_ptr(a_codes, "a_codes", device, u8, (m, k if mode == W4A8 else half)),
-            _ptr(a_scales, "a_scales", device, torch.float32 if mode == W4A8 else u8,
-                 (m,) if mode == W4A8 else mx_scale_shape(m, k)),
-            _ptr(w_codes, "w_codes", device, u8, (n, half)), _ptr(w_scales, "w_scales", device, u8, mx_scale_shape(n, k))]
-    return device, m, n, k, ptrs
+    if mode == W4A8:
+        pa = _ptr(a_codes, "a_codes", dev, u8, (m, k))
+        ps = _ptr(a_scales, "a_scales", dev, torch.float32, (m,))
+    else:
+        pa = _ptr(a_codes, "a_codes", dev, u8, (m, half))
+        ps = _ptr(a_scales, "a_scales", dev, u8, mx_scale_shape(m, k))
+    return dev, m, n, k, pa, ps, _ptr(w_codes, "w_codes", dev, u8, (n, half)), _ptr(w_scales, "w_scales", dev, u8,
+                                                                                    mx_scale_shape(n, k))
 
 
 def gemm_residual(mode, a_codes, a_scales, w_codes, w_scales, residual, bias=None, gate=None, rows_per_group=None,
@@ -227,18 +254,22 @@ def gemm_residual(mode, a_codes, a_scales, w_codes, w_scales, residual, bias=Non
     residual bf16 [M, N]; ``y`` may be residual itself (in place). gate is [N] or [groups, N], float32 or bfloat16,
     row m using vector m // rows_per_group.
     """
-    torch = _torch()
-    device, m, n, k, ptrs = _operands(mode, a_codes, a_scales, w_codes, w_scales)
+    dev, m, n, k, pa, ps, pw, pws = _operands(mode, a_codes, a_scales, w_codes, w_scales)
     bf16 = torch.bfloat16
-    res = _ptr(residual, "residual", device, bf16, (m, n))
-    b = _ptr(bias, "bias", device, bf16, (n,))
-    (g,), mod_type, ld, rpg = _vectors((("gate", gate),), device, m, n, rows_per_group)
-    handle, ctx = _on(device, stream)
+    pr = _ptr(residual, "residual", dev, bf16, (m, n))
+    pb = _ptr(bias, "bias", dev, bf16, (n,))
+    if gate is None:
+        pg, mod_type, ld, rpg = None, 0, n, 0
+    else:
+        (pg,), mod_type, ld, rpg = _vectors((("gate", gate),), dev, m, n, rows_per_group)
+    handle, ctx = _on(dev, stream)
     with ctx:
         if y is None:
-            y = torch.empty((m, n), dtype=bf16, device=device)
-        st = _lib().mxq_gemm_residual(int(mode), *ptrs, b, int(epilogue), res, g, mod_type, ld, rpg,
-                                      _ptr(y, "y", device, bf16, (m, n)), m, n, k, handle)
+            y = torch.empty((m, n), dtype=bf16, device=residual.device)
+            py = y.data_ptr()
+        else:
+            py = _ptr(y, "y", dev, bf16, (m, n))
+        st = _lib().mxq_gemm_residual(mode, pa, ps, pw, pws, pb, epilogue, pr, pg, mod_type, ld, rpg, py, m, n, k, handle)
     _check(st, "gemm_residual")
     return y
 
@@ -248,19 +279,18 @@ def quantize_weight_gated_mxfp4(w_gate, w_up, codes=None, scales=None, stream=No
 
     codes: uint8 [2H, K/2], the rows of the two weights interleaved by 32; scales: uint8 [ceil(K/128), 2H, 4].
     """
-    torch = _torch()
-    device = _device(w_gate, "w_gate")
+    dev = _index(w_gate, "w_gate")
     h, k = _matrix(w_gate, "w_gate")
     bf16, u8 = torch.bfloat16, torch.uint8
-    pg, pu = _ptr(w_gate, "w_gate", device, bf16), _ptr(w_up, "w_up", device, bf16, (h, k))
-    handle, ctx = _on(device, stream)
+    pg, pu = _ptr(w_gate, "w_gate", dev, bf16, (h, k)), _ptr(w_up, "w_up", dev, bf16, (h, k))
+    handle, ctx = _on(dev, stream)
     with ctx:
         if codes is None:
-            codes = torch.empty((2 * h, k // 2), dtype=u8, device=device)
+            codes = torch.empty((2 * h, k // 2), dtype=u8, device=w_gate.device)
         if scales is None:
-            scales = torch.empty(mx_scale_shape(2 * h, k), dtype=u8, device=device)
-        st = _lib().mxq_quantize_weight_gated_mxfp4(pg, pu, h, k, k, _ptr(codes, "codes", device, u8, (2 * h, k // 2)),
-                                                    _ptr(scales, "scales", device, u8, mx_scale_shape(2 * h, k)), handle)
+            scales = torch.empty(mx_scale_shape(2 * h, k), dtype=u8, device=w_gate.device)
+        st = _lib().mxq_quantize_weight_gated_mxfp4(pg, pu, h, k, k, _ptr(codes, "codes", dev, u8, (2 * h, k // 2)),
+                                                    _ptr(scales, "scales", dev, u8, mx_scale_shape(2 * h, k)), handle)
     _check(st, "quantize_weight_gated_mxfp4")
     return codes, scales
 
@@ -272,26 +302,34 @@ def gemm_gated(mode, a_codes, a_scales, w_codes, w_scales, act, bias_gate=None, 
     w_codes, w_scales from quantize_weight_gated_mxfp4. bf16 [M, H] by default; with ``mxfp4_out`` (W4A4; or y_scales
     given) the second projection's MXFP4 activation, (codes, scales), as quantize_act makes it of the bf16 hidden state.
     """
-    torch = _torch()
-    device, m, n, k, ptrs = _operands(mode, a_codes, a_scales, w_codes, w_scales)
+    dev, m, n, k, pa, ps, pw, pws = _operands(mode, a_codes, a_scales, w_codes, w_scales)
     if n % 2 != 0:
         raise ValueError("w_codes must hold the rows of both projections (quantize_weight_gated_mxfp4)")
     h = n // 2
     bf16, u8 = torch.bfloat16, torch.uint8
-    bg, bu = _ptr(bias_gate, "bias_gate", device, bf16, (h,)), _ptr(bias_up, "bias_up", device, bf16, (h,))
-    mxfp4_out = mxfp4_out or y_scales is not None
-    if mxfp4_out and h % 32 != 0:
-        raise ValueError("an MXFP4 hidden state needs a multiple of 32 columns")
-    handle, ctx = _on(device, stream)
+    pg, pu = _ptr(bias_gate, "bias_gate", dev, bf16, (h,)), _ptr(bias_up, "bias_up", dev, bf16, (h,))
+    handle, ctx = _on(dev, stream)
     with ctx:
-        if y is None:
-            y = torch.empty((m, h // 2), dtype=u8, device=device) if mxfp4_out else \
-                torch.empty((m, h), dtype=bf16, device=device)
-        if mxfp4_out and y_scales is None:
-            y_scales = torch.empty(mx_scale_shape(m, h), dtype=u8, device=device)
-        st = _lib().mxq_gemm_gated(int(mode), *ptrs, bg, bu, int(act),
-                                   _ptr(y, "y", device, u8 if mxfp4_out else bf16, (m, h // 2 if mxfp4_out else h)),
-                                   _ptr(y_scales, "y_scales", device, u8, mx_scale_shape(m, h)), m, h, k, handle)
+        if mxfp4_out or y_scales is not None:
+            mxfp4_out = True
+            if y is None:
+                y = torch.empty((m, h // 2), dtype=u8, device=a_codes.device)
+                py = y.data_ptr()
+            else:
+                py = _ptr(y, "y", dev, u8, (m, h // 2))
+            if y_scales is None:
+                y_scales = torch.empty(mx_scale_shape(m, h), dtype=u8, device=a_codes.device)
+                pys = y_scales.data_ptr()
+            else:
+                pys = _ptr(y_scales, "y_scales", dev, u8, mx_scale_shape(m, h))
+        else:
+            pys = None
+            if y is None:
+                y = torch.empty((m, h), dtype=bf16, device=a_codes.device)
+                py = y.data_ptr()
+            else:
+                py = _ptr(y, "y", dev, bf16, (m, h))
+        st = _lib().mxq_gemm_gated(mode, pa, ps, pw, pws, pg, pu, act, py, pys, m, h, k, handle)
     _check(st, "gemm_gated")
     return (y, y_scales) if mxfp4_out else y
 

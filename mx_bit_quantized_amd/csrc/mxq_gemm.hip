@@ -581,6 +581,7 @@ gemm_pipe_kernel(
   constexpr int TM = C::TM, NT = C::NT;
   static_assert(!LRB || (MODE == 0 && KT == 128 && WAVES == 4), "the branch stages take the shape of a W4A4 code stage");
   static_assert(FUSE == kFuseNone || (QOUT < 2 && !LRB && (QOUT == 0 || (MODE == 0 && FUSE == kFuseGated))), "fused forms");
+  static_assert(FUSE != kFuseResidual || WAVES == 4, "residual stages: one wave per SIMD");
   constexpr bool GATED = FUSE == kFuseGated, RES = FUSE == kFuseResidual;
   static_assert(QOUT < 2 || (MODE == 0 && WAVES == 4 && !LRB), "transformed output: W4A4, four waves");
   // ring of NB stage slots, then two tile-parameter blocks: bias slice (512
@@ -2197,9 +2198,8 @@ hipError_t launch_gemm_residual(int mode, const void* a_codes, const void* a_sca
   if (mode == 1)
     return launch_pipe<1, kPipeKT[1], kPipeNB[1], 4, 0, false, kFuseResidual>(
         a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);
-  if (w4a4_eight_waves(M, N, K))
-    return launch_pipe<0, kPipeKT[0], kPipeNB[0], 8, 0, false, kFuseResidual>(
-        a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);
+  // (four waves per workgroup at every size: with eight the stages spill, and
+  // 32760 x 5120 x 5120 took 525 us against 500, 256 x 5120 x 5120 37 against 38)
   return launch_pipe<0, kPipeKT[0], kPipeNB[0], 4, 0, false, kFuseResidual>(
       a_codes, a_scales, w_codes, w_scales, bias, epilogue, y, M, N, K, s, nullptr, nullptr, nullptr, nullptr, 0, nullptr, f);
 }

@@ -175,6 +175,9 @@ class FakeCuda(torch.Tensor):
     is_cuda = property(lambda self: True)
     device = property(lambda self: self.dev)
 
+    def get_device(self):
+        return self.dev.index
+
 
 def fake(*shape, dtype=torch.bfloat16, device="cuda:0"):
     return FakeCuda(torch.zeros(*shape, dtype=dtype), device)
