@@ -18,6 +18,9 @@
 // wave per row, which needs no barrier, would pull them through the L2 for
 // every row. Workgroups take contiguous runs of rows, those of one XCD
 // adjacent, so that the 64-byte pieces of a code panel's lines meet in one L2.
+// 75600 x 5120, layer norm with gate and modulation: 628 us in bf16 (4.93 TB/s
+// over x, branch, h and out; a 2 GiB copy reaches 4.92), MXFP4 544 us (4.65), FP8
+// 601 us (4.51, three reductions a row). One row of 5120: 3.0 - 4.4 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -92,8 +95,13 @@ __device__ __forceinline__ void load_mod8(const void* p, int64_t at, int bf16, f
 
 // x, branch and h carry no __restrict__: h may be either of the two (a thread
 // reads its chunks of a row before it writes them, and no other thread's).
-template <int CH, int R, int OUT>
-__global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
+// POST: with a norm of the branch (its statistics and post_bias). HOLD: the factors
+// stay in registers for all rows of a group, else they are read at their use.
+// AHEAD: the next rows' loads are issued before the arithmetic on the present
+// ones, the first ones' before the factors' (at a group's last rows, whose batch
+// may be cut short, rows are read again). WPE: waves per SIMD to leave room for.
+template <int CH, int R, int OUT, bool POST, bool HOLD, bool AHEAD, int WPE>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(WPE))) void norm_quant_kernel(const NormArgs a) {
   // sums of the workgroup's waves, double-buffered: a reduction's reads are
   // over for every wave before the barrier of the next one, so the buffer is
   // free for the one after that
@@ -142,8 +150,17 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
     for (int i = 0; i < R; ++i) v[i] = row_max(v[i]);
     buf ^= 1;
   };
+  // Several chunks per thread: the values are unpacked again after a reduction
+  // (the compiler would keep all of them in fp32 across it, and spill).
+  auto keep_packed = [](uint4 (&v)[CH][R]) {
+    if constexpr (CH > 1)
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < R; ++i) asm volatile("" : "+v"(v[c][i].x), "+v"(v[c][i].y), "+v"(v[c][i].z), "+v"(v[c][i].w));
+  };
   // mean (layer norm, else 0) and 1 / sqrt(mean square + eps) of R rows of bf16 chunks
-  auto stats = [&](const uint4 (&v)[CH][R], int kind, float (&mu)[R], float (&rs)[R]) {
+  auto stats = [&](uint4 (&v)[CH][R], int kind, float (&mu)[R], float (&rs)[R]) {
 #pragma unroll
     for (int i = 0; i < R; ++i) mu[i] = 0.0f;
     if (kind == MXQ_NORM_LAYER) {
@@ -156,6 +173,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
           mu[i] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
         }
       total(mu);
+      keep_packed(v);
 #pragma unroll
       for (int i = 0; i < R; ++i) mu[i] *= a.inv_k;
     }
@@ -175,6 +193,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
       }
     }
     total(rs);
+    keep_packed(v);
 #pragma unroll
     for (int i = 0; i < R; ++i) rs[i] = 1.0f / __builtin_sqrtf(__builtin_fmaf(rs[i], a.inv_k, a.eps));
   };
@@ -193,12 +212,12 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) gw[e] *= f[e];
     }
-    if (a.post_bias != nullptr) {
+    if (POST && a.post_bias != nullptr) {
       bf16x8_to_f32(*reinterpret_cast<const uint4*>(a.post_bias + col), f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) gb[e] = gw[e] * f[e];
     }
-    if (a.post_weight != nullptr) {
+    if (POST && a.post_weight != nullptr) {
       bf16x8_to_f32(*reinterpret_cast<const uint4*>(a.post_weight + col), f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) gw[e] *= f[e];
@@ -229,11 +248,21 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
     }
   };
 
-  // R > 1: the factors stay in registers for all rows of a group; with one row
-  // at a time they are read at their use (rows few, or too wide to hold both)
-  constexpr bool HOLD = R > 1;
-  float GW[8], GB[8], A[8], B[8];
-  static_assert(!HOLD || CH == 1, "held factors: one chunk per thread");
+  float GW[HOLD ? CH : 1][8], GB[HOLD ? CH : 1][8], A[HOLD ? CH : 1][8], B[HOLD ? CH : 1][8];
+  // rows r .. r + R - 1 (those before `end`) into registers
+  auto load_rows = [&](int64_t r, uint4 (&x)[CH][R], uint4 (&b)[CH][R]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const bool live = r + i < end && ok[c];
+        x[c][i] = live ? *reinterpret_cast<const uint4*>(a.x + (r + i) * a.ldx + at[c]) : make_uint4(0, 0, 0, 0);
+        if (a.branch != nullptr)
+          b[c][i] = live ? *reinterpret_cast<const uint4*>(a.branch + (r + i) * a.ldb + at[c]) : make_uint4(0, 0, 0, 0);
+      }
+  };
+  uint4 xn[CH][R], bn[CH][R];
+  if constexpr (AHEAD) load_rows(begin, xn, bn);
   int64_t base = 0;           // the group's vectors
   int64_t group_end = begin;  // rows from here on need another group's factors
   // (every thread of the workgroup takes the same path: the loop's bounds and
@@ -243,8 +272,11 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
       const int64_t group = a.rows_per_group > 0 ? r0 / a.rows_per_group : 0;
       base = group * a.ld_mod;
       if constexpr (HOLD) {
-        gate_factors(base, at[0], ok[0], GW, GB);
-        norm_factors(base, at[0], ok[0], A, B);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          gate_factors(base, at[c], ok[c], GW[c], GB[c]);
+          norm_factors(base, at[c], ok[c], A[c], B[c]);
+        }
       }
       group_end = a.rows_per_group > 0 ? (group + 1) * a.rows_per_group : a.M;
       group_end = group_end < end ? group_end : end;
@@ -252,15 +284,18 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
     const int nr = (int)(group_end - r0 < R ? group_end - r0 : R);
 
     uint4 h[CH][R], b[CH][R];
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const bool live = i < nr && ok[c];
-        h[c][i] = live ? *reinterpret_cast<const uint4*>(a.x + (r0 + i) * a.ldx + at[c]) : make_uint4(0, 0, 0, 0);
-        if (a.branch != nullptr)
-          b[c][i] = live ? *reinterpret_cast<const uint4*>(a.branch + (r0 + i) * a.ldb + at[c]) : make_uint4(0, 0, 0, 0);
-      }
+        for (int c = 0; c < CH; ++c) {
+          h[c][i] = xn[c][i];
+          b[c][i] = bn[c][i];
+        }
+      load_rows(r0 + nr, xn, bn);
+    } else {
+      load_rows(r0, h, b);
+    }
     float mu[R], rs[R];
     if (a.branch != nullptr) {
 #pragma unroll
@@ -268,10 +303,11 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
         mu[i] = 0.0f;
         rs[i] = 1.0f;
       }
-      if (a.post_norm != MXQ_NORM_NONE) stats(b, a.post_norm, mu, rs);
+      if constexpr (POST) stats(b, a.post_norm, mu, rs);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        if constexpr (!HOLD) gate_factors(base, at[c], ok[c], GW, GB);
+        const int f = HOLD ? c : 0;
+        if constexpr (!HOLD) gate_factors(base, at[c], ok[c], GW[0], GB[0]);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           float fx[8], fb[8];
@@ -279,13 +315,18 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
           bf16x8_to_f32(b[c][i], fb);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float t = __builtin_fmaf((fb[e] - mu[i]) * rs[i], GW[e], GB[e]);
-            fx[e] += ok[c] ? t : 0.0f;
+            if constexpr (POST) {
+              const float t = __builtin_fmaf((fb[e] - mu[i]) * rs[i], GW[f][e], GB[f][e]);
+              fx[e] += ok[c] ? t : 0.0f;
+            } else {
+              fx[e] = __builtin_fmaf(fb[e], GW[f][e], fx[e]);  // zeros past the row's end
+            }
           }
           h[c][i] = make_uint4(bf16x2_rne(fx[0], fx[1]), bf16x2_rne(fx[2], fx[3]), bf16x2_rne(fx[4], fx[5]),
                                bf16x2_rne(fx[6], fx[7]));
           if (a.h != nullptr && i < nr && ok[c]) *reinterpret_cast<uint4*>(a.h + (r0 + i) * a.ldh + at[c]) = h[c][i];
         }
+        if constexpr (CH > 2) __builtin_amdgcn_sched_barrier(0);  // one chunk's values at a time
       }
     }
     stats(h, a.norm, mu, rs);
@@ -296,19 +337,22 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
     for (int i = 0; i < R; ++i) amax[i] = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if constexpr (!HOLD) norm_factors(base, at[c], ok[c], A, B);
+      const int fc = HOLD ? c : 0;
+      if constexpr (!HOLD) norm_factors(base, at[c], ok[c], A[0], B[0]);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         float f[8];
         bf16x8_to_f32(h[c][i], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf((f[e] - mu[i]) * rs[i], A[e], B[e]);
+        for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf((f[e] - mu[i]) * rs[i], A[fc][e], B[fc][e]);
         h[c][i] = make_uint4(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
                              bf16x2_rne(f[6], f[7]));
         if constexpr (OUT == kOutFp8) amax[i] = umax(amax[i], ok[c] ? chunk_amax(h[c][i]) : 0u);
       }
+      if constexpr (CH > 2) __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (OUT == kOutFp8) total_max(amax);
+    keep_packed(h);
 
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -360,19 +404,21 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(const NormArgs a) {
             if (pc == 0) a.out_scales[(int64_t)p * a.M + row] = sb | (s1 << 8) | (s2 << 16) | (s3 << 24);
           }
         }
+        if constexpr (CH > 2) __builtin_amdgcn_sched_barrier(0);
       }
     }
     r0 += nr;
   }
 }
 
-template <int CH, int R>
+template <int CH, int R, bool POST, bool HOLD, bool AHEAD, int WPE>
 static void launch_norm_out(int out, const NormArgs& a, int grid, int threads, hipStream_t s) {
+  const dim3 g(grid), t(threads);
   switch (out) {
-    case kOutMxfp4: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutMxfp4>), dim3(grid), dim3(threads), 0, s, a); break;
-    case kOutFp8: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutFp8>), dim3(grid), dim3(threads), 0, s, a); break;
-    case kOutHadamard: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutHadamard>), dim3(grid), dim3(threads), 0, s, a); break;
-    default: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutBf16>), dim3(grid), dim3(threads), 0, s, a); break;
+    case kOutMxfp4: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutMxfp4, POST, HOLD, AHEAD, WPE>), g, t, 0, s, a); break;
+    case kOutFp8: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutFp8, POST, HOLD, AHEAD, WPE>), g, t, 0, s, a); break;
+    case kOutHadamard: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutHadamard, POST, HOLD, AHEAD, WPE>), g, t, 0, s, a); break;
+    default: hipLaunchKernelGGL((norm_quant_kernel<CH, R, kOutBf16, POST, HOLD, AHEAD, WPE>), g, t, 0, s, a); break;
   }
 }
 
@@ -411,18 +457,31 @@ hipError_t launch_norm_quant(int mode, const mxq_norm_args& g, hipStream_t s) {
   const int chunks = a.K >> 3;
   const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
   const int threads = (chunks + 64 * ch - 1) / (64 * ch) * 64;
-  const int R = 4;
-  const int64_t max_wgs = 1024;
-  const bool many = ch == 1 && g.M >= R * max_wgs;
-  const int step = many ? R : 1;
-  int64_t per = (g.M + max_wgs - 1) / max_wgs;
-  per = (per + step - 1) / step * step;
+  const int waves = threads >> 6;
+  // about 20 waves per CU in one round of workgroups, so that the factors are read
+  // as seldom as the chip can be filled (75600 x 5120: 512 workgroups 625 us, 1024
+  // 670 us; 20000 x 512, one wave each: 5120 workgroups 14 us, 1024 25 us)
+  const int64_t wgs = 256 * (20 / waves > 0 ? 20 / waves : 1);
+  const int64_t per = (g.M + wgs - 1) / wgs;
   a.rows_per_wg = per;
   const int grid = (int)((g.M + per - 1) / per);
-  if (many) launch_norm_out<1, R>(out, a, grid, threads, s);
-  else if (ch == 1) launch_norm_out<1, 1>(out, a, grid, threads, s);
-  else if (ch == 2) launch_norm_out<2, 1>(out, a, grid, threads, s);
-  else launch_norm_out<4, 1>(out, a, grid, threads, s);
+  const bool post = g.post_norm != MXQ_NORM_NONE;
+  // Two rows at a time fill the 128-byte lines of a code panel in one workgroup
+  // (MXFP4 75600 x 5120: 539 us against 585); with few rows per workgroup one row,
+  // its loads issued ahead of the factors' (2048 x 5120: 14.9 us against 16.2); with
+  // the branch's statistics one row, two would not fit the registers.
+  if (ch == 1) {
+    if (post) launch_norm_out<1, 1, true, true, false, 5>(out, a, grid, threads, s);
+    else if (per >= 8) launch_norm_out<1, 2, false, true, false, 5>(out, a, grid, threads, s);
+    else launch_norm_out<1, 1, false, true, true, 5>(out, a, grid, threads, s);
+  } else if (ch == 2) {
+    if (post) launch_norm_out<2, 1, true, true, false, 4>(out, a, grid, threads, s);
+    else launch_norm_out<2, 1, false, true, false, 4>(out, a, grid, threads, s);
+  } else {
+    // (four chunks per thread and their factors do not fit: read at their use)
+    if (post) launch_norm_out<4, 1, true, false, false, 4>(out, a, grid, threads, s);
+    else launch_norm_out<4, 1, false, false, false, 4>(out, a, grid, threads, s);
+  }
   return hipGetLastError();
 }
 
