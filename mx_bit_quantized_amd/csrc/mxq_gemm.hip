@@ -23,6 +23,7 @@
 // over K is the same set of products as in natural order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <math.h>
 #include <stdlib.h>
 
 #include <array>
@@ -2171,17 +2172,43 @@ hipError_t launch_gemm_lowrank(const void* a_codes, const void* a_scales, const 
                                                              y, M, N, K, s, nullptr, nullptr, t, l2, (int)r);
 }
 
-// ---- the operators around the product (FUSE): few rows go to the split-K kernel
-constexpr int64_t kBlockMinRows = 65;
+// ---- the operators around the product (FUSE)
+
+// Whether the pipelined kernel is the faster one, from what both were measured to
+// take (us, one MI355X). Its workgroups take 256 x 256 outputs of the product, one
+// per CU and round; a round takes c + d per 128 elements of K, whether the tiles
+// fill the chip or not (residual, W4A4: 256 x 5120 x 5120 38 us, x 13824 84 us, 1024
+// x 5120 x 5120 40 us). The split-K kernel's take 64 x 32 (64 x 64 of the gated
+// pair), a round of 256 of them a + b per 128 elements (the same shapes: 20, 43 and
+// 71 us). W4A8 and gated figures in the same way, at K = 1024 to 13824.
+static bool pipe_pays(bool gated, int mode, int64_t M, int64_t cols, int64_t K) {
+  static const struct { double a, b, c, d; } kCost[2][2] = {
+      {{2.6, 0.135, 11.2, 0.67}, {3.2, 0.30, 13.0, 0.93}},   // residual: W4A4, W4A8
+      {{3.3, 0.175, 7.5, 0.70}, {3.5, 0.33, 11.5, 1.00}}};   // gated
+  const auto& t = kCost[gated ? 1 : 0][mode];
+  const double panels = (double)(K / 128);
+  const double pipe_tiles = (double)((M + 255) / 256) * (double)(((gated ? 2 : 1) * cols + 255) / 256);
+  const double token_tiles = (double)((M + 63) / 64) * (double)((cols + 31) / 32);
+  return ceil(pipe_tiles / 256) * (t.c + t.d * panels) < ceil(token_tiles / 256) * (t.a + t.b * panels);
+}
+
+// MXQ_BLOCK_KERNEL=pipe or tokens fixes the choice where the pipelined kernel takes
+// the shape (read at every call, so tests can run either kernel on any shape).
+static bool take_pipe(bool gated, int mode, int64_t M, int64_t cols, int64_t K) {
+  const char* v = getenv("MXQ_BLOCK_KERNEL");
+  if (v != nullptr && (v[0] == 'p' || v[0] == 't')) return v[0] == 'p';
+  return M > 32 && pipe_pays(gated, mode, M, cols, K);
+}
 
 bool gemm_residual_pipelined(int mode, int64_t M, int64_t N, int64_t K, const ResidualEpi& e) {
   // gate vectors are read 8 columns at a time
   const bool gate_ok = e.gate == nullptr || e.rows_per_group == 0 || e.ld_mod % 8 == 0;
-  return gate_ok && use_lds(mode, M, N, K, kBlockMinRows);
+  return gate_ok && use_lds(mode, M, N, K, 1) && take_pipe(false, mode, M, N, K);
 }
 
 bool gemm_gated_pipelined(int mode, int64_t M, int64_t H, int64_t K, bool mxfp4_out) {
-  return use_lds(mode, M, 2 * H, K, kBlockMinRows) && (!mxfp4_out || (H % 128 == 0 && mxfp4_out_fits(M, H)));
+  return use_lds(mode, M, 2 * H, K, 1) && (!mxfp4_out || (H % 128 == 0 && mxfp4_out_fits(M, H))) &&
+         take_pipe(true, mode, M, H, K);
 }
 
 hipError_t launch_gemm_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes,

@@ -6,8 +6,8 @@
 // and does little else: it is bound by how fast the whole chip pulls that
 // stream in. A workgroup owns 32 output columns (for the gated pair the 32
 // gate rows and 32 up rows of the same hidden columns, adjacent in the packed
-// weight) and its 8 waves split K: wave w takes the 128-element code panels
-// w, w + 8, ... A wave's load of a panel's 32 rows is 2 KiB of consecutive
+// weight) and its waves (8 or 16) split K: wave w of W takes the 128-element code panels
+// w, w + W, ... A wave's load of a panel's 32 rows is 2 KiB of consecutive
 // memory, kBatch panels are in flight per wave, and nothing goes through LDS on
 // the way to the matrix cores: no row is shared between waves. The tokens are
 // the MFMA's second operand, 32 at a time, from L2; rows past M repeat the last
@@ -15,6 +15,8 @@
 // in wave order, so a result depends on the shape only.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "mxq_block.h"
 #include "mxq_convert.h"
@@ -26,8 +28,6 @@ namespace mxq {
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef float v16f_t __attribute__((ext_vector_type(16)));
 
-constexpr int kTokWaves = 8;   // waves per workgroup, each with every eighth panel
-constexpr int kTokBatch = 4;   // panels loaded before the first MFMA on them
 constexpr int kTokPitch = 36;  // floats per token of a staged 32 x 32 tile (16-byte aligned, banks spread)
 
 // One lane's operands of a panel for a 32-row tile: lane (r, g) holds blocks
@@ -91,12 +91,12 @@ struct TokArgs {
 };
 
 // TM: 32-token tiles per workgroup, which share each load of the weight.
-template <int MODE, int TM, int KIND>
-__global__ __launch_bounds__(64 * kTokWaves) void gemm_tokens_kernel(const TokArgs a) {
+template <int MODE, int TM, int KIND, int WAVES, int BATCH, int WPE>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WPE))) void gemm_tokens_kernel(const TokArgs a) {
   constexpr bool GATED = KIND != kTokResidual;
   constexpr int TN = GATED ? 2 : 1;
   constexpr int XC = MODE == 0 ? 2 : 4;
-  __shared__ __attribute__((aligned(16))) float red[kTokWaves][32 * kTokPitch];
+  __shared__ __attribute__((aligned(16))) float red[WAVES][32 * kTokPitch];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 31, g = lane >> 5;
   const int n0 = blockIdx.x * 32;
@@ -122,12 +122,12 @@ __global__ __launch_bounds__(64 * kTokWaves) void gemm_tokens_kernel(const TokAr
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
-  for (int p0 = wave; p0 < n_panels; p0 += kTokWaves * kTokBatch) {
-    TokFrag<2> wf[kTokBatch][TN];
-    TokFrag<XC> xf[kTokBatch][TM];
+  for (int p0 = wave; p0 < n_panels; p0 += WAVES * BATCH) {
+    TokFrag<2> wf[BATCH][TN];
+    TokFrag<XC> xf[BATCH][TM];
 #pragma unroll
-    for (int u = 0; u < kTokBatch; ++u) {
-      const int p = p0 + kTokWaves * u;
+    for (int u = 0; u < BATCH; ++u) {
+      const int p = p0 + WAVES * u;
       if (p < n_panels) {  // the same for the whole wave
 #pragma unroll
         for (int i = 0; i < TN; ++i) tok_load_fp4(wf[u][i], a.wq, a.ws, w_rows, wrow[i], p, a.K, g);
@@ -141,8 +141,8 @@ __global__ __launch_bounds__(64 * kTokWaves) void gemm_tokens_kernel(const TokAr
       }
     }
 #pragma unroll
-    for (int u = 0; u < kTokBatch; ++u) {
-      if (p0 + kTokWaves * u < n_panels) {
+    for (int u = 0; u < BATCH; ++u) {
+      if (p0 + WAVES * u < n_panels) {
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -166,8 +166,9 @@ __global__ __launch_bounds__(64 * kTokWaves) void gemm_tokens_kernel(const TokAr
   }
 
   // Tile by tile through LDS: wave w's 32 x 32 sums as [token][column], then
-  // thread t adds the 8 waves' for token t / 16, columns 2 (t % 16), + 1.
-  const int tm = threadIdx.x >> 4, tn = (threadIdx.x & 15) * 2;
+  // thread t < 512 adds the waves' for token t / 16, columns 2 (t % 16), + 1.
+  const bool adds = threadIdx.x < 512;
+  const int tm = adds ? threadIdx.x >> 4 : 0, tn = (threadIdx.x & 15) * 2;
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     float v[TN][2];
@@ -181,14 +182,14 @@ __global__ __launch_bounds__(64 * kTokWaves) void gemm_tokens_kernel(const TokAr
       __syncthreads();
       v[i][0] = v[i][1] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kTokWaves; ++w) {
+      for (int w = 0; w < WAVES; ++w) {
         const float2 s = *reinterpret_cast<const float2*>(&red[w][tm * kTokPitch + tn]);
         v[i][0] += s.x;
         v[i][1] += s.y;
       }
     }
     const int64_t m = (int64_t)m0 + 32 * j + tm;
-    const bool live = m < a.M;  // whole 16-lane rows at once: the block maximum below stays uniform
+    const bool live = adds && m < a.M;  // whole 16-lane rows at once: the block maximum below stays uniform
     const int n = n0 + tn;
     if constexpr (MODE == 1) {
       const float s = live ? static_cast<const float*>(a.as)[m] : 0.0f;
@@ -269,11 +270,33 @@ __global__ __launch_bounds__(64 * kTokWaves) void gemm_tokens_kernel(const TokAr
 template <int MODE, int KIND>
 static hipError_t launch_tokens_kind(const TokArgs& a, hipStream_t s) {
   const unsigned gx = (unsigned)(((int64_t)a.N + 31) / 32), gy = (unsigned)(((int64_t)a.M + 63) / 64);
+  auto go = [&](auto tm, auto waves, auto batch, auto wpe) {
+    constexpr int TM = decltype(tm)::value, W = decltype(waves)::value;
+    hipLaunchKernelGGL((gemm_tokens_kernel<MODE, TM, KIND, W, decltype(batch)::value, decltype(wpe)::value>),
+                       dim3(gx, TM == 1 ? 1 : (gy < 65535u ? gy : 65535u)), dim3(64 * W), 0, s, a);
+  };
+  constexpr std::integral_constant<int, 1> c1;
+  constexpr std::integral_constant<int, 2> c2;
+  constexpr std::integral_constant<int, 4> c4;
+  constexpr std::integral_constant<int, 8> c8;
+  constexpr std::integral_constant<int, 16> c16;
+  // Loads in flight come from waves or from panels per wave. One token tile: the
+  // narrow outputs of a residual product (160 workgroups at N = 5120) take 16
+  // waves of one panel (W4A4 1 x 5120 x 13824: 9.1 us, 8 waves of two 10.6), the
+  // gated pair 8 waves of one, two workgroups to a CU (1 x 13824 x 5120: 15.3 us, 4.9
+  // TB/s; three panels and one workgroup 16.6). Two token tiles, whose sums take
+  // the registers: 8 waves, two panels, but one where the residual product has
+  // several tiles of rows (64 rows: 15.4 us against 19.3, 128 rows: 29.1 against 25.4).
   if (a.M <= 32) {
-    hipLaunchKernelGGL((gemm_tokens_kernel<MODE, 1, KIND>), dim3(gx, 1), dim3(64 * kTokWaves), 0, s, a);
+    if constexpr (KIND == kTokResidual) go(c1, c16, c1, c4);
+    else go(c1, c8, c1, c4);
   } else {
-    hipLaunchKernelGGL((gemm_tokens_kernel<MODE, 2, KIND>), dim3(gx, gy < 65535u ? gy : 65535u), dim3(64 * kTokWaves),
-                       0, s, a);
+    if constexpr (KIND == kTokResidual) {
+      if (a.M > 64) go(c2, c8, c1, c2);
+      else go(c2, c8, c2, c2);
+    } else {
+      go(c2, c8, c2, c2);
+    }
   }
   return hipGetLastError();
 }

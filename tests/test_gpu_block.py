@@ -12,6 +12,8 @@ step) relative to the value:
   Their slopes are below 1.2.
 """
 
+import contextlib
+import os
 import sys
 
 import numpy as np
@@ -81,6 +83,24 @@ def within(got, want, tol, what):
     over = (got - want).abs() - tol
     assert over.max() <= 0, f"{what}: off by {float((got - want).abs().max())}, {int((over > 0).sum())} past tolerance, " \
                             f"worst at {np.unravel_index(int(over.argmax()), tuple(over.shape))}"
+
+
+@contextlib.contextmanager
+def block_kernel(name):
+    """The products' kernel fixed to the split-K ("tokens") or the pipelined one ("pipe") where it takes the shape."""
+    old = os.environ.get("MXQ_BLOCK_KERNEL")
+    os.environ["MXQ_BLOCK_KERNEL"] = name
+    try:
+        yield
+    finally:
+        if old is None:
+            os.environ.pop("MXQ_BLOCK_KERNEL", None)
+        else:
+            os.environ["MXQ_BLOCK_KERNEL"] = old
+
+
+# mode, waves of the W4A4 pipelined kernel, kernel
+KERNELS = [(mxq.W4A4, 4, "pipe"), (mxq.W4A4, 8, "pipe"), (mxq.W4A4, 4, "tokens"), (mxq.W4A8, 4, "pipe"), (mxq.W4A8, 4, "tokens")]
 
 
 # ------------------------------------------------------------------- norm ----
@@ -314,6 +334,8 @@ RESIDUAL_CASES = [
     (515, 776, 1280, True, True, torch.bfloat16, 200),
     (1030, 512, 512, False, False, torch.float32, None),
     (700, 300, 736, True, False, torch.float32, 350),
+    (1, 256, 384, True, False, None, None),
+    (40, 1032, 896, True, False, torch.bfloat16, 3),
     # more tiles than workgroups: a workgroup goes from one tile to the next
     (4100, 4360, 512, True, False, torch.float32, 1500),
     (4200, 4104, 640, False, False, torch.bfloat16, 3),
@@ -321,10 +343,10 @@ RESIDUAL_CASES = [
 ]
 
 
-@pytest.mark.parametrize("mode, waves", [(mxq.W4A4, 4), (mxq.W4A4, 8), (mxq.W4A8, 4)])
+@pytest.mark.parametrize("mode, waves, kernel", [k for k in KERNELS if k[1] == 4])
 @pytest.mark.parametrize("case", RESIDUAL_CASES, ids=lambda c: "x".join(map(str, c[:3])))
-def test_gemm_residual_matches_float64(case, mode, waves):
-    with w4a4_waves(waves):
+def test_gemm_residual_matches_float64(case, mode, waves, kernel):
+    with w4a4_waves(waves), block_kernel(kernel):
         check_residual(case, mode)
 
 
@@ -376,10 +398,10 @@ GATED_CASES = [
 ]
 
 
-@pytest.mark.parametrize("mode, waves", [(mxq.W4A4, 4), (mxq.W4A4, 8), (mxq.W4A8, 4)])
+@pytest.mark.parametrize("mode, waves, kernel", KERNELS)
 @pytest.mark.parametrize("case", GATED_CASES, ids=lambda c: "x".join(map(str, c[:3])))
-def test_gemm_gated_matches_float64(case, mode, waves):
-    with w4a4_waves(waves):
+def test_gemm_gated_matches_float64(case, mode, waves, kernel):
+    with w4a4_waves(waves), block_kernel(kernel):
         check_gated(case, mode)
 
 
@@ -422,10 +444,15 @@ def test_gated_weight_packing_interleaves_the_rows(h, k):
     assert_codes_equal(host_u8(scales), host_u8(rs), "scales")
 
 
-@pytest.mark.parametrize("mode", [mxq.W4A4, mxq.W4A8])
+@pytest.mark.parametrize("mode, waves, kernel", KERNELS)
 @pytest.mark.parametrize("m", [1, 40, 270])
-def test_products_write_their_rows_only(mode, m):
+def test_products_write_their_rows_only(mode, waves, kernel, m):
     """Rows before and after the output keep their values."""
+    with w4a4_waves(waves), block_kernel(kernel):
+        check_rows(mode, m)
+
+
+def check_rows(mode, m):
     n, k = 256, 512
     g = gen(m)
     a, w, _, _ = quantized(mode, g, m, n, k)
