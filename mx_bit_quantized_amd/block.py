@@ -192,7 +192,7 @@ def norm_quantize(mode, x, branch=None, gate=None, branch_scale=1.0, post_norm=N
             pb, ldb = _rows(branch, "branch", dev, (m, k))
             if write_h:
                 if h is None:
-                    h = torch.empty((m, k), dtype=bf16, device=x.device)
+                    h = torch.empty_like(x) if ldx == k else torch.empty((m, k), dtype=bf16, device=x.device)
                     ph = h.data_ptr()
                 else:
                     ph, ldh = _rows(h, "h", dev, (m, k))
@@ -205,7 +205,7 @@ def norm_quantize(mode, x, branch=None, gate=None, branch_scale=1.0, post_norm=N
         pos = None
         if mode == POLICY_BF16:
             if out is None:
-                out = torch.empty((m, k), dtype=bf16, device=x.device)
+                out = torch.empty_like(x) if ldx == k else torch.empty((m, k), dtype=bf16, device=x.device)
                 po = out.data_ptr()
             else:
                 po = _ptr(out, "out", dev, bf16, (m, k))
@@ -265,7 +265,7 @@ def gemm_residual(mode, a_codes, a_scales, w_codes, w_scales, residual, bias=Non
     handle, ctx = _on(dev, stream)
     with ctx:
         if y is None:
-            y = torch.empty((m, n), dtype=bf16, device=residual.device)
+            y = torch.empty_like(residual)
             py = y.data_ptr()
         else:
             py = _ptr(y, "y", dev, bf16, (m, n))

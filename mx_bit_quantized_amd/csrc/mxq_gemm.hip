@@ -559,16 +559,16 @@ struct FuseArgs {
 // GELU chooses the activation (tanh-GELU, else SiLU).
 //
 // FUSE = kFuseResidual: y = residual + gate * epi(sum + bias), rounded once. After
-// a tile's code stages come four residual stages: the residual tile's bf16 columns
-// 32 q .. (the wn = 0 half) ride in the W role of stage q and columns 128 + 32 q ..
-// (wn = 1) in the X role, 64 bytes per token row, so the copies run ahead through
-// the ring like any others and no load waits in the epilogue, where its wait
-// would also drain the copies in flight (vmcnt counts them in order). The residual
-// stages are the tile's epilogue: in stage q each wave finishes, rounds and stores
-// its column tiles i = q, and the next tile's first stage carries none. (With the
-// sums finished in place and left to the ordinary epilogue, the accumulators went
-// through the vector unit twice: W4A4 32760 x 5120 x 5120 took 513 us against
-// mxq_gemm's 415.)
+// a tile's code stages come four residual stages: token rows 32 q .. 32 q + 31 of
+// the tile's upper half (the wm = 0 waves') ride in the W role of stage q, those of
+// its lower half (wm = 1) in the X role, 512 bytes a row, so the copies run ahead
+// through the ring like any others and no load waits in the epilogue, where its
+// wait would also drain the copies in flight (vmcnt counts them in order). The
+// residual stages are the tile's epilogue: in stage q each wave finishes, rounds
+// and stores its row group j = q, and the next tile's first stage carries none.
+// (With the sums finished in place and left to the ordinary epilogue, the
+// accumulators went through the vector unit twice: W4A4 32760 x 5120 x 5120 took
+// 513 us against mxq_gemm's 415.)
 template <int MODE, int KT, int NB, bool GELU, bool BIAS, int QOUT, bool LRB, int WAVES, int FUSE>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES / 4, WAVES / 4))) void
 gemm_pipe_kernel(
@@ -666,17 +666,21 @@ gemm_pipe_kernel(
 #pragma unroll
     for (int q = 0; q < C::X_INSTR; ++q) vxl[q] = vx[q] / C::X_RB * lr_pitch + vx[q] % C::X_RB;
   }
-  // residual stages: 64 bytes of a token row of the output's row pitch (the FP8
-  // X role has rows of 128 bytes: its upper halves copy nothing)
+  // Residual stages: LDS rows of 512 bytes (256 columns of a token), two per copy;
+  // 16-byte chunk c of row `row` lies at chunk c ^ row, so that the 32 lanes that
+  // read one chunk of 32 rows hit 32 different ones. (The FP8 X role is twice as
+  // large: waves 2 and 3 copy nothing there.)
   uint32_t vwr[RES ? C::W_INSTR : 1], vxr[RES ? C::X_INSTR : 1];
   if constexpr (RES) {
 #pragma unroll
-    for (int q = 0; q < C::W_INSTR; ++q) vwr[q] = vw[q] / C::W_RB * ((uint32_t)N * 2u) + vw[q] % C::W_RB;
+    for (int q = 0; q < C::W_INSTR; ++q) {
+      const uint32_t row = (uint32_t)((wave * C::W_INSTR + q) * 2 + g);
+      vwr[q] = row * ((uint32_t)N * 2u) + (((uint32_t)r ^ row) * 16u);
+    }
 #pragma unroll
     for (int q = 0; q < C::X_INSTR; ++q) {
-      int row, c;
-      unswz<C::X_RB>((wave * C::X_INSTR + q) * 64 + lane, row, c);
-      vxr[q] = c < 4 ? (uint32_t)row * ((uint32_t)N * 2u) + (uint32_t)c * 16u + 256u : 0x80000000u;
+      const uint32_t row = (uint32_t)((wave * C::X_INSTR + q) * 2 + g);
+      vxr[q] = row < 32 ? (row + 128u) * ((uint32_t)N * 2u) + (((uint32_t)r ^ row) * 16u) : 0x80000000u;
     }
   }
   const uint32_t w_panel = (uint32_t)N * C::W_RB;  // bytes of one code panel
@@ -778,7 +782,7 @@ gemm_pipe_kernel(
   // gate reads as zeros). The X scales' place stays unused.
   auto issue_residual = [&](int q, int slot, int rq, const i32x4& rr, const i32x4& rg) {
     const uint32_t base = lds_ring + (uint32_t)slot * C::STAGE;
-    const uint32_t so = cp_nb * 2u + (uint32_t)rq * 64u;
+    const uint32_t so = cp_nb * 2u + (uint32_t)rq * ((uint32_t)N * 64u);  // 32 rows a stage
     if (q < C::W_INSTR) {
       lds_dma16(rr, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, vwr[q] + so);
     } else if (q < C::W_INSTR + C::X_INSTR) {
@@ -1797,17 +1801,18 @@ gemm_pipe_kernel(
       run_stage_x(tile_k, s_in, first_tag, br_tag, issue_one);
     };
 
-    // Residual stage Q (RES): for the wave's column tiles i = Q
+    // Residual stage Q (RES): for the wave's row group j = Q
     //   y = residual + gate * epi(acc (* token scale) + bias),
     // the residual from the stage's slot, in the accumulators' layout: the lane's
-    // 4 columns 8 t + 4 g .. of row group j's row r are 8 bytes of that row's
-    // chunk t. All LDS reads, those of the next stage's first fragments too, are
-    // issued before the arithmetic (one wave per SIMD has nothing else to cover
-    // their latency with), the copies in the first half, and row group j's tile
-    // leaves through the staging area while group j + 1 is computed: 2 stores of
-    // 16 rows x 64 bytes, all of them after the stage's last copy. ROWS: a gate
-    // vector per row (a tile with rows of several groups), from memory; else the
-    // tile's one vector from the slot, or none.
+    // 4 columns 8 t + 4 g .. of column tile i of row r are 8 bytes of the row's chunk
+    // 16 wn + 4 i + t. The residual is read two tiles ahead, the next stage's
+    // first fragments before the arithmetic (one wave per SIMD has nothing else
+    // to cover their latency with), the copies in the first half, and the tiles
+    // leave through the staging area while the next ones are computed: W4A4 in
+    // pairs, 4 stores of 8 rows x 128 bytes, W4A8, whose area holds one tile, 2 stores
+    // of 16 rows x 64 bytes each; all of them after the stage's last copy. ROWS: a
+    // gate vector per row (a tile with rows of several groups), from memory; else
+    // the tile's one vector from the slot, or none.
     auto run_residual_stage = [&](int tile_k, auto q_tag, auto rows_tag, int row_t, int col_t, const i32x4& ry, auto&& copy) {
       constexpr int Q = decltype(q_tag)::value;
       constexpr bool ROWS = decltype(rows_tag)::value;
@@ -1819,118 +1824,138 @@ gemm_pipe_kernel(
       const uint8_t* here = ring + slot * C::STAGE;
       const uint8_t* next = ring + slot_next * C::STAGE;
       const uint8_t* prm = ring + PARAM_OFF + (tile_k & 1) * PARAM_BYTES;
-      const int wcol = wn * 128 + 32 * Q;  // the wave's first column in the tile, and per lane + 8 t + 4 g
-      uint2 rv[TM][4];
+      uint2 rv[4][4];
+      // (chunk ^ r of row r, as one exclusive or per read; opaque, or all 16 offsets
+      // are kept in registers through the code stages)
+      uint32_t lane_at = (uint32_t)(r * 512 + (r << 4) + 8 * g) ^ (uint32_t)(wn << 8);
+      asm volatile("" : "+v"(lane_at));
+      const uint8_t* rows = here + (wm == 0 ? C::W_OFF : C::X_OFF);
+      auto read_residual = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < TM; ++j)
+        for (int t2 = 0; t2 < 4; ++t2)
+          rv[i][t2] = *reinterpret_cast<const uint2*>(rows + (lane_at ^ (uint32_t)((4 * i + t2) << 4)));
+      };
+      read_residual(0);
+      read_residual(1);
+      const bool gated = !ROWS && fuse.gate != nullptr;
+      float sm = 1.0f;
+      if constexpr (MODE == 1) sm = *reinterpret_cast<const float*>(prm + P_TOK + (xrow0 + 32 * Q) * 4);
+      // gate and bias of tile i, read one tile ahead
+      uint2 bb[4];
+      uint4 gq[4];  // 4 fp32, or 4 bf16 in the first half
+      const int row_q = row_t + xrow0 + 32 * Q;
+      const int64_t at0 = ROWS && row_q < M ? (int64_t)(row_q / fuse.rows_per_group) * fuse.ld_mod : 0;
+      auto read_factors = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
         for (int t2 = 0; t2 < 4; ++t2) {
-          const int lrow = xrow0 + 32 * j;
-          const uint32_t off = wn == 0 ? C::W_OFF + swz<C::W_RB>(lrow, t2) : C::X_OFF + swz<C::X_RB>(lrow, t2);
-          rv[j][t2] = *reinterpret_cast<const uint2*>(here + off + 8 * g);
-        }
-      const bool gated = !ROWS && fuse.gate != nullptr;
-      float gt[16], bs[16], sm[TM];
-#pragma unroll
-      for (int t2 = 0; t2 < 4; ++t2) {
-        if constexpr (BIAS) {
-          const uint2 v = *reinterpret_cast<const uint2*>(prm + P_BIAS + (wcol + 8 * t2 + 4 * g) * 2);
-          bs[4 * t2] = as_float(v.x << 16);
-          bs[4 * t2 + 1] = as_float(v.x & 0xFFFF0000u);
-          bs[4 * t2 + 2] = as_float(v.y << 16);
-          bs[4 * t2 + 3] = as_float(v.y & 0xFFFF0000u);
-        }
-        if constexpr (!ROWS) {
-          // both widths are read (a choice of loads would be a branch), then chosen
-          const uint2 h = *reinterpret_cast<const uint2*>(here + C::WS_OFF + (wcol + 8 * t2 + 4 * g) * 2);
-          const float4 f = *reinterpret_cast<const float4*>(here + C::WS_OFF + (wcol + 8 * t2 + 4 * g) * 4);
-          const float hb[4] = {as_float(h.x << 16), as_float(h.x & 0xFFFF0000u), as_float(h.y << 16),
-                               as_float(h.y & 0xFFFF0000u)};
-          const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) gt[4 * t2 + c] = gated ? (fuse.mod_bf16 ? hb[c] : ff[c]) : 1.0f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        sm[j] = 1.0f;
-        if constexpr (MODE == 1) sm[j] = *reinterpret_cast<const float*>(prm + P_TOK + (xrow0 + 32 * j) * 4);
-      }
-#pragma unroll
-      for (int k = 0; k < STAGE_ITEMS; ++k) read_item(next, 0, 0, kStageOrder[OI][k], cur, cur_sc);
-      // the tiles read first come from the last code step's first MFMAs; the
-      // waits of a VALU read of an MFMA result are spelled out all the same
-      // (the compiler does not see through the asm reads)
-      asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-      uint4 rd[2];
-      auto tile_store = [&](int j) {
-        const int col = col_t + wcol + (lane & 3) * 8;
-        const uint32_t bad = col < N ? 0u : 0x80000000u;
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const int row = wm * 32 * TM + 32 * j + 16 * st + (lane >> 2);
-          buf_store16(ry, (((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u) | bad, rd[st]);
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        if constexpr (ROWS) {
-          const int row = row_t + xrow0 + 32 * j;
-          const int64_t at0 = row < M ? (int64_t)(row / fuse.rows_per_group) * fuse.ld_mod : 0;
-#pragma unroll
-          for (int t2 = 0; t2 < 4; ++t2) {
-            const int col = min(col_t + wcol + 8 * t2 + 4 * g, N - 4);  // (columns past N are not stored)
+          const int col = wn * 128 + 32 * i + 8 * t2 + 4 * g;  // in the tile
+          if constexpr (BIAS) bb[t2] = *reinterpret_cast<const uint2*>(prm + P_BIAS + col * 2);
+          if constexpr (ROWS) {
+            const int n = min(col_t + col, N - 4);  // (columns past N are not stored)
             if (fuse.mod_bf16) {
-              const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(fuse.gate) + at0 + col);
-              gt[4 * t2] = as_float(v.x << 16);
-              gt[4 * t2 + 1] = as_float(v.x & 0xFFFF0000u);
-              gt[4 * t2 + 2] = as_float(v.y << 16);
-              gt[4 * t2 + 3] = as_float(v.y & 0xFFFF0000u);
+              const uint2 h2 = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(fuse.gate) + at0 + n);
+              gq[t2].x = h2.x;
+              gq[t2].y = h2.y;
             } else {
-              const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(fuse.gate) + at0 + col);
-              gt[4 * t2] = v.x;
-              gt[4 * t2 + 1] = v.y;
-              gt[4 * t2 + 2] = v.z;
-              gt[4 * t2 + 3] = v.w;
+              gq[t2] = *reinterpret_cast<const uint4*>(static_cast<const float*>(fuse.gate) + at0 + n);
+            }
+          } else if (gated) {
+            if (fuse.mod_bf16) {
+              const uint2 h2 = *reinterpret_cast<const uint2*>(here + C::WS_OFF + col * 2);
+              gq[t2].x = h2.x;
+              gq[t2].y = h2.y;
+            } else {
+              gq[t2] = *reinterpret_cast<const uint4*>(here + C::WS_OFF + col * 4);
             }
           }
         }
+      };
+#pragma unroll
+      for (int t2 = 0; t2 < 4; ++t2) {
+        bb[t2] = make_uint2(0u, 0u);
+        gq[t2] = make_uint4(0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u);  // no gate: ones
+      }
+      read_factors(0);
+#pragma unroll
+      for (int k = 0; k < STAGE_ITEMS; ++k) read_item(next, 0, 0, kStageOrder[OI][k], cur, cur_sc);
+      // the row groups' last MFMAs are long over but for the last step's; the waits
+      // of a VALU read of an MFMA result are spelled out all the same (the compiler
+      // does not see through the asm reads)
+      asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      const bool bf = (ROWS || gated) && fuse.mod_bf16;
+      uint32_t even[4][2];
+      uint4 rd[MODE == 0 ? 4 : 2];
+      // byte offset of the lane's first store in the tile's rows, + 2 N a row, + 128
+      // bytes a pair or 64 a tile (opaque: 32 ready offsets would fill the registers)
+      constexpr int S_ROWS = MODE == 0 ? 8 : 16, S_LANES = 64 / S_ROWS;
+      const int s_col = wn * 128 + (lane % S_LANES) * 8;
+      uint32_t st_at = (uint32_t)(wm * 128 + lane / S_LANES) * ((uint32_t)N * 2u) + (uint32_t)s_col * 2u;
+      asm volatile("" : "+v"(st_at));
+      // MODE 0: the pair k (tiles 2k, 2k + 1) of row group Q; MODE 1: tile k
+      auto tiles_store = [&](int k) __attribute__((always_inline)) {
+        const uint32_t bad = col_t + s_col + S_LANES * 8 * k < N ? 0u : 0x80000000u;
+#pragma unroll
+        for (int st = 0; st < 32 / S_ROWS; ++st) {
+          const uint32_t so = (uint32_t)(32 * Q + S_ROWS * st) * ((uint32_t)N * 2u) + (uint32_t)(col_t + S_LANES * 8 * k) * 2u;
+          buf_store16(ry, (st_at + so) | bad, rd[st]);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         uint32_t pk[4][2];
 #pragma unroll
         for (int t2 = 0; t2 < 4; ++t2) {
           float o[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float v;
-            if constexpr (WAVES == 4) v = acc_read(acc[Q][j][4 * t2 + c]);
-            else v = acc[Q][j][4 * t2 + c];
-            const uint32_t r2 = c < 2 ? rv[j][t2].x : rv[j][t2].y;
-            if constexpr (MODE == 1) v = BIAS ? __builtin_fmaf(v, sm[j], bs[4 * t2 + c]) : v * sm[j];
-            else if constexpr (BIAS) v += bs[4 * t2 + c];
+            float v = acc_read(acc[i][Q][4 * t2 + c]);
+            const uint32_t r2 = c < 2 ? rv[i][t2].x : rv[i][t2].y;
+            const uint32_t b2 = c < 2 ? bb[t2].x : bb[t2].y;
+            const uint32_t g2 = c < 2 ? gq[t2].x : gq[t2].y;
+            const float b = as_float(c & 1 ? b2 & 0xFFFF0000u : b2 << 16);
+            const uint32_t g4 = c == 0 ? gq[t2].x : c == 1 ? gq[t2].y : c == 2 ? gq[t2].z : gq[t2].w;
+            const float gt = as_float(bf ? (c & 1 ? g2 & 0xFFFF0000u : g2 << 16) : g4);
+            if constexpr (MODE == 1) v = BIAS ? __builtin_fmaf(v, sm, b) : v * sm;
+            else if constexpr (BIAS) v += b;
             if constexpr (GELU) v = gelu_tanh_dev(v);
-            o[c] = __builtin_fmaf(gt[4 * t2 + c], v, as_float(c & 1 ? r2 & 0xFFFF0000u : r2 << 16));
+            o[c] = __builtin_fmaf(gt, v, as_float(c & 1 ? r2 & 0xFFFF0000u : r2 << 16));
           }
           pk[t2][0] = pack_bf16x2(o[0], o[1]);
           pk[t2][1] = pack_bf16x2(o[2], o[3]);
-          constexpr int STEPS = 2 * TM;  // the copies go out in the first half
-          if (j < TM / 2) {
+          if (i < 2) {  // the copies go out in the first half
 #pragma unroll
-            for (int q = (4 * j + t2) * C::PER_WAVE / STEPS; q < (4 * j + t2 + 1) * C::PER_WAVE / STEPS; ++q)
-              copy(q, slot_refill);
+            for (int q = (4 * i + t2) * C::PER_WAVE / 8; q < (4 * i + t2 + 1) * C::PER_WAVE / 8; ++q) copy(q, slot_refill);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-        // (with two row groups the last copies follow the first group's arithmetic,
-        // so its tile, too, leaves after them)
-        if (j > 0) tile_store(j - 1);
-        ev8_write(pk);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        ev8_read(rd);
-        // the next tile's writes stay behind these reads
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (i < 3) read_factors(i + 1);
+        if (i < 2) read_residual(i + 2);
+        if constexpr (MODE == 0) {
+          if (i & 1) {
+            ev_unit_write(even, pk);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            ev_unit_read(rd);
+            // the next pair's writes stay behind these reads
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          } else {
+            if (i == 2) tiles_store(0);
+#pragma unroll
+            for (int t2 = 0; t2 < 4; ++t2) {
+              even[t2][0] = pk[t2][0];
+              even[t2][1] = pk[t2][1];
+            }
+          }
+        } else {
+          if (i > 0) tiles_store(i - 1);
+          ev8_write(pk);
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          ev8_read(rd);
+          // the next tile's writes stay behind these reads
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
       }
-      tile_store(TM - 1);
+      tiles_store(MODE == 0 ? 1 : 3);
       advance_cursor();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       slot = slot_next;
