@@ -379,12 +379,30 @@ __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
 // the kernel orders it explicitly with s_waitcnt vmcnt + s_barrier. It has no
 // register result, so nothing the compiler allocates can be overwritten while
 // it is in flight; M0 needs one wait state before the copy reads it.
+// A vector memory instruction must not read a scalar register in the 5 wait states
+// after a VALU instruction wrote it (v_readfirstlane, and v_readlane where the
+// compiler brings a spilled resource back); the compiler keeps that distance for
+// its own instructions, not in front of an asm block. FAR blocks keep it
+// themselves: in the fused forms, whose resources do not all stay in registers,
+// everything but the code stages' copies (there a tile's last stores went astray
+// without it). Those copies keep their resources, and the wait would cost them
+// 3%: a test reads the distance off the built code.
+template <bool FAR = false>
 __device__ __forceinline__ void lds_dma16(const i32x4& rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  if constexpr (FAR)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
 }
+template <bool FAR = false>
 __device__ __forceinline__ void lds_dma4(const i32x4& rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  if constexpr (FAR)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
 }
 
@@ -465,8 +483,8 @@ __device__ __forceinline__ void buf_store4(const i32x4& rs, uint32_t voff, uint3
 }
 
 // Range-checked 2-byte store of the low half of v.
-__device__ __forceinline__ void buf_store2(const i32x4& rs, uint32_t voff, uint32_t v) {
-  asm volatile("buffer_store_short %0, %1, %2, 0 offen" :: "v"(v), "v"(voff), "s"(rs) : "memory");
+__device__ __forceinline__ void buf_store2(const i32x4& rs, uint32_t voff, uint32_t v) {  // (FAR)
+  asm volatile("s_nop 4\n\tbuffer_store_short %0, %1, %2, 0 offen" :: "v"(v), "v"(voff), "s"(rs) : "memory");
 }
 
 // E8M0 scale byte of a 32-column block of one row from the lane's 8 bf16 pairs
@@ -509,9 +527,13 @@ __device__ __forceinline__ void buf_store8(const i32x4& rs, uint32_t voff, uint3
   asm volatile("buffer_store_dwordx2 %0, %1, %2, 0 offen" :: "v"(d), "v"(voff), "s"(rs) : "memory");
 }
 
+template <bool FAR = false>
 __device__ __forceinline__ void buf_store16(const i32x4& rs, uint32_t voff, const uint4& v) {
   const i32x4 d = {(int)v.x, (int)v.y, (int)v.z, (int)v.w};
-  asm volatile("buffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1" :: "v"(d), "v"(voff), "s"(rs) : "memory");
+  if constexpr (FAR)
+    asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1" :: "v"(d), "v"(voff), "s"(rs) : "memory");
+  else
+    asm volatile("buffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1" :: "v"(d), "v"(voff), "s"(rs) : "memory");
 }
 
 // Operators fused around the product (FUSE, below).
@@ -584,6 +606,7 @@ gemm_pipe_kernel(
   static_assert(FUSE == kFuseNone || (QOUT < 2 && !LRB && (QOUT == 0 || (MODE == 0 && FUSE == kFuseGated))), "fused forms");
   static_assert(FUSE != kFuseResidual || WAVES == 4, "residual stages: one wave per SIMD");
   constexpr bool GATED = FUSE == kFuseGated, RES = FUSE == kFuseResidual;
+  constexpr bool FAR = FUSE != kFuseNone;  // see lds_dma16
   static_assert(QOUT < 2 || (MODE == 0 && WAVES == 4 && !LRB), "transformed output: W4A4, four waves");
   // ring of NB stage slots, then two tile-parameter blocks: bias slice (512
   // bytes), a sink for the unused waves' copies (512), token scales (1024, FP8)
@@ -614,7 +637,10 @@ gemm_pipe_kernel(
   const int KB = K >> 5;
   const uint32_t w_row = (uint32_t)K >> 1;
   const uint32_t x_row = MODE == 0 ? ((uint32_t)K >> 1) : (uint32_t)K;
-  const int nq = K / KT;                                   // code stages of a tile
+  // code stages of a tile (the fused forms take any K: a last, ragged panel has a
+  // stage of its own, see issue_tail)
+  const int nq = FUSE == kFuseNone ? K / KT : (K + KT - 1) / KT;
+  const int scale_blocks = FUSE == kFuseNone ? KB : 4 * nq;  // per row, padded to whole groups
   const int n_stages = nq + (LRB ? (lr_rank >> 5) : RES ? 4 : 0);   // + the branch's rank panels, the residual's columns
   const int NY = GATED ? N >> 1 : N;                       // columns of the output
 
@@ -666,23 +692,6 @@ gemm_pipe_kernel(
 #pragma unroll
     for (int q = 0; q < C::X_INSTR; ++q) vxl[q] = vx[q] / C::X_RB * lr_pitch + vx[q] % C::X_RB;
   }
-  // Residual stages: LDS rows of 512 bytes (256 columns of a token), two per copy;
-  // 16-byte chunk c of row `row` lies at chunk c ^ row, so that the 32 lanes that
-  // read one chunk of 32 rows hit 32 different ones. (The FP8 X role is twice as
-  // large: waves 2 and 3 copy nothing there.)
-  uint32_t vwr[RES ? C::W_INSTR : 1], vxr[RES ? C::X_INSTR : 1];
-  if constexpr (RES) {
-#pragma unroll
-    for (int q = 0; q < C::W_INSTR; ++q) {
-      const uint32_t row = (uint32_t)((wave * C::W_INSTR + q) * 2 + g);
-      vwr[q] = row * ((uint32_t)N * 2u) + (((uint32_t)r ^ row) * 16u);
-    }
-#pragma unroll
-    for (int q = 0; q < C::X_INSTR; ++q) {
-      const uint32_t row = (uint32_t)((wave * C::X_INSTR + q) * 2 + g);
-      vxr[q] = row < 32 ? (row + 128u) * ((uint32_t)N * 2u) + (((uint32_t)r ^ row) * 16u) : 0x80000000u;
-    }
-  }
   const uint32_t w_panel = (uint32_t)N * C::W_RB;  // bytes of one code panel
   const uint32_t x_stage = MODE == 0 ? (uint32_t)M * C::X_RB : (uint32_t)C::X_RB;
   // Scales (group-major, 128-element groups): the tile's 256 dwords of group
@@ -706,8 +715,8 @@ gemm_pipe_kernel(
   // Whole-operand buffer resources: rows past M or N fall outside them.
   const i32x4 rw = make_rsrc(wq, w_row * (uint32_t)N);
   const i32x4 rx = make_rsrc(aq, x_row * (uint32_t)M);
-  const i32x4 rws = make_rsrc(ws, (uint32_t)KB * (uint32_t)N);
-  const i32x4 rxs = make_rsrc(asc, MODE == 0 ? (uint32_t)KB * (uint32_t)M : 0u);
+  const i32x4 rws = make_rsrc(ws, (uint32_t)scale_blocks * (uint32_t)N);
+  const i32x4 rxs = make_rsrc(asc, MODE == 0 ? (uint32_t)scale_blocks * (uint32_t)M : 0u);
   const i32x4 rl2 = make_rsrc(lr_l2, lr_pitch * (uint32_t)N);
   const i32x4 rlt = make_rsrc(lr_t, lr_pitch * (uint32_t)M);
   const i32x4 rsc = wave < 4 ? rws : rxs;  // eight waves: this wave's scale operand
@@ -776,22 +785,57 @@ gemm_pipe_kernel(
       lds_dma4(rxs, base + C::XS_OFF + wave * 256, vs + so);
     }
   };
+  // Copy q of a ragged last panel (the cursor's tile and stage; fused forms): its
+  // rows hold K % 128 elements, and chunks past them read as zeros. Weight chunks
+  // of zeros null whatever the activation has there.
+  auto issue_tail = [&](int q, int slot) __attribute__((always_inline)) {
+    if (q >= C::W_INSTR + C::X_INSTR) {
+      issue_one(q, slot);  // scale groups are whole: padded with zero bytes
+      return;
+    }
+    const uint32_t base = lds_ring + (uint32_t)slot * C::STAGE;
+    const uint32_t tail = (uint32_t)(K % KT);
+    if (q < C::W_INSTR) {
+      const uint32_t row = vw[q] / C::W_RB, at = vw[q] % C::W_RB;
+      const uint32_t so = cp_nb * (tail >> 1) + (uint32_t)cp_s * w_panel;
+      lds_dma16<FAR>(rw, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024,
+                at < (tail >> 1) ? row * (tail >> 1) + at + so : 0x80000000u);
+    } else {
+      const int qx = q - C::W_INSTR;
+      int row, c;
+      unswz<C::X_RB>((wave * C::X_INSTR + qx) * 64 + lane, row, c);
+      const uint32_t tb = MODE == 0 ? tail >> 1 : tail, pitch = MODE == 0 ? tb : x_row;
+      const uint32_t so = cp_mb * pitch + (uint32_t)cp_s * x_stage;
+      lds_dma16<FAR>(rx, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024,
+                (uint32_t)c * 16u < tb ? (uint32_t)row * pitch + (uint32_t)c * 16u + so : 0x80000000u);
+    }
+  };
   // Copy q of residual stage rq of the cursor's tile (RES) into ring slot `slot`:
   // rr the tile's residual rows, rg the tile's slice of its gate vector, which
   // takes the place of the W scales (256 fp32 or, in half the bytes, bf16; no
   // gate reads as zeros). The X scales' place stays unused.
+  // LDS rows hold 512 bytes (256 columns of a token), two per copy; 16-byte chunk c
+  // of row `row` lies at chunk c ^ row, so that the 32 lanes that read one chunk of
+  // 32 rows hit 32 different ones. (The FP8 X role is twice as large: waves 2 and 3
+  // copy nothing there.) The lane's offset is formed per copy, from an opaque value:
+  // kept ready, the offsets would fill the registers of all code stages.
   auto issue_residual = [&](int q, int slot, int rq, const i32x4& rr, const i32x4& rg) {
     const uint32_t base = lds_ring + (uint32_t)slot * C::STAGE;
     const uint32_t so = cp_nb * 2u + (uint32_t)rq * ((uint32_t)N * 64u);  // 32 rows a stage
+    uint32_t half = (uint32_t)g;
+    asm volatile("" : "+v"(half));
     if (q < C::W_INSTR) {
-      lds_dma16(rr, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, vwr[q] + so);
+      const uint32_t row = (uint32_t)((wave * C::W_INSTR + q) * 2) + half;
+      lds_dma16<FAR>(rr, base + C::W_OFF + (wave * C::W_INSTR + q) * 1024, row * ((uint32_t)N * 2u) + (((uint32_t)r ^ row) << 4) + so);
     } else if (q < C::W_INSTR + C::X_INSTR) {
       const int qx = q - C::W_INSTR;
-      lds_dma16(rr, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, vxr[qx] + so);
+      const uint32_t row = (uint32_t)((wave * C::X_INSTR + qx) * 2) + half;
+      const uint32_t off = (row + 128u) * ((uint32_t)N * 2u) + (((uint32_t)r ^ row) << 4) + so;
+      lds_dma16<FAR>(rr, base + C::X_OFF + (wave * C::X_INSTR + qx) * 1024, row < 32 ? off : 0x80000000u);
     } else if (q == C::W_INSTR + C::X_INSTR && wave < 4) {
-      lds_dma4(rg, base + C::WS_OFF + wave * 256, (uint32_t)(wave * 256 + lane * 4));
+      lds_dma4<FAR>(rg, base + C::WS_OFF + wave * 256, (uint32_t)(wave * 256 + lane * 4));
     } else {
-      lds_dma4(rxs, base + C::XS_OFF + (wave & 3) * 256, 0x80000000u);
+      lds_dma4<FAR>(rxs, base + C::XS_OFF + (wave & 3) * 256, 0x80000000u);
     }
   };
   auto advance_cursor = [&] {
@@ -822,20 +866,20 @@ gemm_pipe_kernel(
       const uint32_t hb = nb >> 1;
       const uint16_t* src = wave == 0 ? bias : fuse.bias_up;
       const i32x4 rb = make_rsrc(src + hb, src != nullptr ? ((uint32_t)NY - hb) * 2u : 0u);
-      lds_dma4(rb, pb + (wave < 2 ? P_BIAS + wave * 256 : P_SINK + ((wave - 2) & 1) * 256),
+      lds_dma4<FAR>(rb, pb + (wave < 2 ? P_BIAS + wave * 256 : P_SINK + ((wave - 2) & 1) * 256),
                live && wave < 2 ? (uint32_t)(lane * 4) : 0x80000000u);
     } else {
       const i32x4 rb = make_rsrc(bias + nb, bias != nullptr ? ((uint32_t)N - nb) * 2u : 0u);
-      lds_dma4(rb, pb + (wave < 2 ? P_BIAS + wave * 256 : P_SINK + ((wave - 2) & 1) * 256),
+      lds_dma4<FAR>(rb, pb + (wave < 2 ? P_BIAS + wave * 256 : P_SINK + ((wave - 2) & 1) * 256),
                live && wave < 2 ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
     }
     if constexpr (MODE == 1) {
       const i32x4 rt = make_rsrc(static_cast<const uint8_t*>(asc) + mb * 4u, ((uint32_t)M - mb) * 4u);
-      lds_dma4(rt, pb + P_TOK + wave * 256, live ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
+      lds_dma4<FAR>(rt, pb + P_TOK + wave * 256, live ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
     }
     if constexpr (QOUT == 2) {
       const i32x4 rm = make_rsrc(out_mult + nb, ((uint32_t)N - nb) * 4u);
-      lds_dma4(rm, pb + P_MULT + wave * 256, live ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
+      lds_dma4<FAR>(rm, pb + P_MULT + wave * 256, live ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u);
     }
   };
 
@@ -1148,7 +1192,8 @@ gemm_pipe_kernel(
     static_assert(!RES || WAIT_BASE + R_WAIT2 <= 63, "vmcnt range");
     int slot = 0;  // ring slot of the stage being computed
     // `copy(q, slot)` issues the stage's copies (those of the stage D ahead)
-    auto run_stage_x = [&](int tile_k, int s_in, auto first_tag, auto br_tag, auto&& copy) {
+    // (the stages must be inlined: a call would put the accumulators into memory)
+    auto run_stage_x = [&](int tile_k, int s_in, auto first_tag, auto br_tag, auto&& copy) __attribute__((always_inline)) {
       constexpr bool FIRST = decltype(first_tag)::value;
       constexpr bool BR = decltype(br_tag)::value;
       if (tile_k > 0 || s_in > 0) {
@@ -1218,7 +1263,7 @@ gemm_pipe_kernel(
           const int m_q = ptm * 256 + wm * 32 * TM;
           const int h_q = ptn * 128 + wn * 64;  // first hidden column of the wave
           const i32x4 rq = make_rsrc(y, (uint32_t)M * (uint32_t)NY / 2u);
-          const i32x4 rsq = make_rsrc(y_scales, (uint32_t)(NY >> 7) * (uint32_t)M * 4u);
+          const i32x4 rsq = make_rsrc(y_scales, (uint32_t)((NY + 127) >> 7) * (uint32_t)M * 4u);
           float sm[MODE == 1 ? TM : 1];
           if constexpr (MODE == 1) {
 #pragma unroll
@@ -1235,18 +1280,21 @@ gemm_pipe_kernel(
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
               const int row = wm * 32 * TM + 32 * j + 16 * st + (lane >> 2);
-              buf_store16(ry, (((uint32_t)row * (uint32_t)NY + (uint32_t)col) * 2u) | bad, rd[st]);
+              buf_store16<FAR>(ry, (((uint32_t)row * (uint32_t)NY + (uint32_t)col) * 2u) | bad, rd[st]);
             }
           };
+          // (a last panel of fewer than 128 columns has narrower rows; its blocks past
+          // NY write their zero scale bytes and no codes)
           auto group_store = [&](int j) {
-            const uint32_t bad = ev_live && h_q < NY ? 0u : 0x80000000u;
-            const uint32_t pan = (uint32_t)(h_q >> 7);
+            const uint32_t live = ev_live && 128 * ptn < NY ? 0u : 0x80000000u;
+            const uint32_t pan = (uint32_t)ptn;
+            const uint32_t pitch = (uint32_t)min(128, NY - 128 * ptn) >> 1;
             const int row = m_q + 32 * j + (lane >> 1);
-            const uint32_t off = (pan * (uint32_t)M + (uint32_t)row) * 64u + (uint32_t)(wn * 32 + (lane & 1) * 16);
-            buf_store16(rq, row < M ? (off | bad) : 0x80000000u, rd[0]);
+            const uint32_t off = pan * (uint32_t)M * 64u + (uint32_t)row * pitch + (uint32_t)(wn * 32 + (lane & 1) * 16);
+            buf_store16<FAR>(rq, row < M && h_q + 32 * (lane & 1) < NY ? (off | live) : 0x80000000u, rd[0]);
             const int srow = m_q + 32 * j + r;
             const uint32_t soff = (pan * (uint32_t)M + (uint32_t)srow) * 4u + (uint32_t)(wn * 2);
-            buf_store2(rsq, g == 0 && srow < M ? (soff | bad) : 0x80000000u, sbs_done);
+            buf_store2(rsq, g == 0 && srow < M ? (soff | live) : 0x80000000u, sbs_done);
           };
           auto beforeg = [&](int sl) __attribute__((always_inline)) {
             const int i = sl & 3, j = sl >> 2;
@@ -1276,7 +1324,7 @@ gemm_pipe_kernel(
             }
             if constexpr (QOUT) {
               if (i & 1) {
-                const uint32_t sb = tile_block_scale(pk, g);
+                const uint32_t sb = h_q + 32 * (i >> 1) < NY ? tile_block_scale(pk, g) : 0u;
                 const uint2 w = tile_codes(pk, sb);
                 *reinterpret_cast<uint2*>(ev_region + r * QP + 16 * (i >> 1) + 8 * g) = w;
                 sbs |= sb << (8 * (i >> 1));
@@ -1797,7 +1845,7 @@ gemm_pipe_kernel(
       slot = slot_next;
     };
 
-    auto run_stage = [&](int tile_k, int s_in, auto first_tag, auto br_tag) {
+    auto run_stage = [&](int tile_k, int s_in, auto first_tag, auto br_tag) __attribute__((always_inline)) {
       run_stage_x(tile_k, s_in, first_tag, br_tag, issue_one);
     };
 
@@ -1813,7 +1861,8 @@ gemm_pipe_kernel(
     // of 16 rows x 64 bytes each; all of them after the stage's last copy. ROWS: a
     // gate vector per row (a tile with rows of several groups), from memory; else
     // the tile's one vector from the slot, or none.
-    auto run_residual_stage = [&](int tile_k, auto q_tag, auto rows_tag, int row_t, int col_t, const i32x4& ry, auto&& copy) {
+    auto run_residual_stage = [&](int tile_k, auto q_tag, auto rows_tag, int row_t, int col_t, const i32x4& ry,
+                                  auto&& copy) __attribute__((always_inline)) {
       constexpr int Q = decltype(q_tag)::value;
       constexpr bool ROWS = decltype(rows_tag)::value;
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(WAIT_BASE + (Q == 0 ? 0 : Q == 1 ? R_WAIT1 : R_WAIT2)));
@@ -1898,7 +1947,7 @@ gemm_pipe_kernel(
 #pragma unroll
         for (int st = 0; st < 32 / S_ROWS; ++st) {
           const uint32_t so = (uint32_t)(32 * Q + S_ROWS * st) * ((uint32_t)N * 2u) + (uint32_t)(col_t + S_LANES * 8 * k) * 2u;
-          buf_store16(ry, (st_at + so) | bad, rd[st]);
+          buf_store16<FAR>(ry, (st_at + so) | bad, rd[st]);
         }
       };
 #pragma unroll
@@ -1961,6 +2010,16 @@ gemm_pipe_kernel(
       slot = slot_next;
     };
 
+    // Code stages 1 .. end - 1 of a tile (fused forms), end = nq - D (or 1 for none): the
+    // last of them copies the tile's last panel, which may be ragged. (Loops without
+    // iterations, no branches: see below.)
+    [[maybe_unused]] auto code_stages = [&](int tile_k, int end) __attribute__((always_inline)) {
+      const int plain = K % KT != 0 && end > 1 ? end - 1 : end;
+      for (int s_in = 1; s_in < plain; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
+      for (int s_in = plain; s_in < end; ++s_in)
+        run_stage_x(tile_k, s_in, std::false_type{}, std::false_type{}, issue_tail);
+    };
+
     // one more first stage after the last tile: it carries that tile's
     // epilogue (its own MFMAs work on zeros); the loop test is the only exit,
     // at the end of an iteration, so no path leaves between a first stage's
@@ -1981,8 +2040,8 @@ gemm_pipe_kernel(
         // stage): code stages nq - D .. nq - 1 copy residual stages 0 .. D - 1 of
         // their own tile, residual stage Q copies residual stage Q + D or, past the
         // last, the next tile's first code stages.
-        if (tile_k < count) {
-          for (int s_in = 1; s_in < nq - D; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
+        {
+          code_stages(tile_k, nq - D);
           int ctm = 0, ctn = 0;
           tile_of(first + tile_k * stride, tiles_m, tiles_n, ctm, ctn);
           const int row_t = ctm * 256, col_t = ctn * 256;
@@ -2019,6 +2078,11 @@ gemm_pipe_kernel(
           if (gate_kind == 2) residual_stages(std::true_type{});
           else residual_stages(std::false_type{});
         }
+      } else if constexpr (GATED) {
+        const int c_end = tile_k < count ? nq - D : 1, q_end = tile_k < count ? nq : 1;
+        code_stages(tile_k, c_end);
+        for (int s_in = c_end > 1 ? c_end : 1; s_in < q_end; ++s_in)
+          run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
       } else {
         for (int s_in = 1; s_in < s_end; ++s_in) run_stage(tile_k, s_in, std::false_type{}, std::false_type{});
       }
@@ -2211,7 +2275,7 @@ static bool pipe_pays(bool gated, int mode, int64_t M, int64_t cols, int64_t K) 
       {{2.6, 0.135, 11.2, 0.67}, {3.2, 0.30, 13.0, 0.93}},   // residual: W4A4, W4A8
       {{3.3, 0.175, 7.5, 0.70}, {3.5, 0.33, 11.5, 1.00}}};   // gated
   const auto& t = kCost[gated ? 1 : 0][mode];
-  const double panels = (double)(K / 128);
+  const double panels = (double)((K + 127) / 128);
   const double pipe_tiles = (double)((M + 255) / 256) * (double)(((gated ? 2 : 1) * cols + 255) / 256);
   const double token_tiles = (double)((M + 63) / 64) * (double)((cols + 31) / 32);
   return ceil(pipe_tiles / 256) * (t.c + t.d * panels) < ceil(token_tiles / 256) * (t.a + t.b * panels);
@@ -2225,14 +2289,21 @@ static bool take_pipe(bool gated, int mode, int64_t M, int64_t cols, int64_t K) 
   return M > 32 && pipe_pays(gated, mode, M, cols, K);
 }
 
+// The pipelined kernel's shapes in the fused forms: any rows, any K of enough
+// stages (one more when the last is ragged: it is copied in a stage after the first).
+static bool block_lds(int mode, int64_t M, int64_t N, int64_t K) {
+  const int64_t kt = kPipeKT[mode], up = (K + kt - 1) / kt * kt;
+  return use_lds(mode, M, N, up, 1) && (K == up || K / kt >= kPipeNB[mode]);
+}
+
 bool gemm_residual_pipelined(int mode, int64_t M, int64_t N, int64_t K, const ResidualEpi& e) {
   // gate vectors are read 8 columns at a time
   const bool gate_ok = e.gate == nullptr || e.rows_per_group == 0 || e.ld_mod % 8 == 0;
-  return gate_ok && use_lds(mode, M, N, K, 1) && take_pipe(false, mode, M, N, K);
+  return gate_ok && block_lds(mode, M, N, K) && take_pipe(false, mode, M, N, K);
 }
 
 bool gemm_gated_pipelined(int mode, int64_t M, int64_t H, int64_t K, bool mxfp4_out) {
-  return use_lds(mode, M, 2 * H, K, 1) && (!mxfp4_out || (H % 128 == 0 && mxfp4_out_fits(M, H))) &&
+  return block_lds(mode, M, 2 * H, K) && (!mxfp4_out || mxfp4_out_fits(M, H)) &&
          take_pipe(true, mode, M, H, K);
 }
 

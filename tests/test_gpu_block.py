@@ -336,6 +336,10 @@ RESIDUAL_CASES = [
     (700, 300, 736, True, False, torch.float32, 350),
     (1, 256, 384, True, False, None, None),
     (40, 1032, 896, True, False, torch.bfloat16, 3),
+    # a last panel of 32, 64 and 96 elements
+    (300, 264, 672, True, False, torch.float32, None),
+    (70, 776, 832, False, True, torch.bfloat16, 64),
+    (4100, 4104, 736, True, False, torch.float32, 4000),
     # more tiles than workgroups: a workgroup goes from one tile to the next
     (4100, 4360, 512, True, False, torch.float32, 1500),
     (4200, 4104, 640, False, False, torch.bfloat16, 3),
@@ -392,6 +396,11 @@ GATED_CASES = [
     (515, 416, 1280, True, False, mxq.GATED_GELU_TANH),
     (1030, 640, 512, False, True, mxq.GATED_SILU),
     (350, 160, 736, True, True, mxq.GATED_SILU),
+    # a last panel of 32, 64 and 96 elements, of K and of the hidden state
+    (300, 288, 672, True, False, mxq.GATED_SILU),
+    (70, 192, 832, False, True, mxq.GATED_GELU_TANH),
+    (259, 352, 736, True, True, mxq.GATED_SILU),
+    (4100, 2144, 1120, False, False, mxq.GATED_SILU),
     # more tiles than workgroups: a workgroup goes from one tile to the next
     (4100, 2176, 512, True, True, mxq.GATED_SILU),
     (4200, 2080, 640, False, False, mxq.GATED_GELU_TANH),
