@@ -603,3 +603,54 @@ def test_empty_problems_write_nothing():
         assert y.shape == (0, 64)
         assert mxq.gemm_gated(mode, codes, scales, *wg, mxq.GATED_SILU).shape == (0, 64)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("mode", [mxq.W4A4, mxq.W4A8])
+def test_outputs_past_2_gib(mode):
+    """The last rows of outputs larger than 2^31 bytes equal the same rows computed alone by the same kernel."""
+    m, n, k, last = 140000, 8192, 512, 300
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    w = mxq.quantize_weight_mxfp4((0.05 * torch.randn(n, k, generator=g, device=DEV)).to(torch.bfloat16))
+    wg = mxq.quantize_weight_gated_mxfp4(*((0.05 * torch.randn(n, k, generator=g, device=DEV)).to(torch.bfloat16) for _ in range(2)))
+    a, a_last = mxq.quantize_act(mode, x), mxq.quantize_act(mode, x[-last:].contiguous())
+    gate = torch.randn(2, n, generator=g, device=DEV)
+    residual = torch.randn(m, n, generator=g, device=DEV, dtype=torch.bfloat16)
+    assert 2 * m * n > 2 ** 31
+    for kernel in ("pipe", "tokens"):
+        with block_kernel(kernel):
+            say("past 2 GiB", mode, kernel)
+            y = mxq.gemm_residual(mode, *a, *w, residual, gate=gate, rows_per_group=m - last)
+            part = mxq.gemm_residual(mode, *a_last, *w, residual[-last:], gate=gate[1:])
+            assert torch.equal(y[-last:], part)
+            del y
+            hid = mxq.gemm_gated(mode, *a, *wg, mxq.GATED_SILU)
+            assert torch.equal(hid[-last:], mxq.gemm_gated(mode, *a_last, *wg, mxq.GATED_SILU))
+            del hid
+    h = mxq.norm_quantize(mxq.POLICY_BF16, residual, branch=residual, norm=mxq.NORM_LAYER, h=residual)[0]
+    tail = residual[-last:].clone()  # h, in place: twice the residual
+    assert torch.equal(h[-last:], mxq.norm_quantize(mxq.POLICY_BF16, tail, norm=mxq.NORM_LAYER)[0])
+
+
+def test_check_finite_refuses_and_reports(monkeypatch):
+    monkeypatch.setenv("MXQ_CHECK_FINITE", "1")
+    k = 512
+    w = mxq.quantize_weight_mxfp4(bf16(randn(gen(1), 256, k)).to(DEV))
+    x = bf16(randn(gen(2), 5, k)).to(DEV)
+    bad = x.clone()
+    bad[3, 7] = float("inf")
+    out = torch.full((5, k), 7.0, dtype=torch.bfloat16, device=DEV)
+    for kw in ({"x": bad}, {"x": x, "branch": bad}):
+        with pytest.raises(mxq.MxqError) as e:
+            mxq.norm_quantize(mxq.POLICY_BF16, out=out, **kw)
+        assert e.value.status == mxq.ERR_NONFINITE and (out == 7).all()
+    a = mxq.quantize_act(mxq.W4A4, x)
+    res = torch.zeros(5, 256, dtype=torch.bfloat16, device=DEV)
+    assert torch.isfinite(mxq.gemm_residual(mxq.W4A4, *a, *w, res)).all()
+    res[4, 255] = float("nan")
+    y = torch.full_like(res, 7.0)
+    with pytest.raises(mxq.MxqError) as e:
+        mxq.gemm_residual(mxq.W4A4, *a, *w, res, y=y)
+    assert e.value.status == mxq.ERR_NONFINITE and (y == 7).all()
+    with pytest.raises(mxq.MxqError):
+        mxq.quantize_weight_gated_mxfp4(bad.new_full((32, k), float("inf")), bad.new_zeros((32, k)))
