@@ -2267,18 +2267,20 @@ hipError_t launch_gemm_lowrank(const void* a_codes, const void* a_scales, const 
 // take (us, one MI355X). Its workgroups take 256 x 256 outputs of the product, one
 // per CU and round; a round takes c + d per 128 elements of K, whether the tiles
 // fill the chip or not (residual, W4A4: 256 x 5120 x 5120 38 us, x 13824 84 us, 1024
-// x 5120 x 5120 40 us). The split-K kernel's take 64 x 32 (64 x 64 of the gated
-// pair), a round of 256 of them a + b per 128 elements (the same shapes: 20, 43 and
-// 71 us). W4A8 and gated figures in the same way, at K = 1024 to 13824.
+// x 5120 x 5120 40 us). 512 of the split-K kernel's 32 x 32 pieces of a residual
+// product, or 256 of its 64 x 32 pairs, take a + b per 128 elements (the same shapes:
+// 18, 41 and about 70 us). W4A8 and gated figures in the same way, at K = 1024 to 13824.
 static bool pipe_pays(bool gated, int mode, int64_t M, int64_t cols, int64_t K) {
   static const struct { double a, b, c, d; } kCost[2][2] = {
-      {{2.6, 0.135, 11.2, 0.67}, {3.2, 0.30, 13.0, 0.93}},   // residual: W4A4, W4A8
+      {{1.9, 0.134, 11.2, 0.67}, {2.6, 0.28, 13.0, 0.93}},   // residual: W4A4, W4A8
       {{3.3, 0.175, 7.5, 0.70}, {3.5, 0.33, 11.5, 1.00}}};   // gated
   const auto& t = kCost[gated ? 1 : 0][mode];
   const double panels = (double)((K + 127) / 128);
   const double pipe_tiles = (double)((M + 255) / 256) * (double)(((gated ? 2 : 1) * cols + 255) / 256);
-  const double token_tiles = (double)((M + 63) / 64) * (double)((cols + 31) / 32);
-  return ceil(pipe_tiles / 256) * (t.c + t.d * panels) < ceil(token_tiles / 256) * (t.a + t.b * panels);
+  const double token_cols = (double)((cols + 31) / 32);
+  const double token_rounds = gated ? ceil((double)((M + 63) / 64) * token_cols / 256)
+                                    : fmax(1.0, (double)((M + 31) / 32) * token_cols / 512);
+  return ceil(pipe_tiles / 256) * (t.c + t.d * panels) < token_rounds * (t.a + t.b * panels);
 }
 
 // MXQ_BLOCK_KERNEL=pipe or tokens fixes the choice where the pipelined kernel takes

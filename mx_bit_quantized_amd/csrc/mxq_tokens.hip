@@ -269,34 +269,33 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WPE)
 
 template <int MODE, int KIND>
 static hipError_t launch_tokens_kind(const TokArgs& a, hipStream_t s) {
-  const unsigned gx = (unsigned)(((int64_t)a.N + 31) / 32), gy = (unsigned)(((int64_t)a.M + 63) / 64);
-  auto go = [&](auto tm, auto waves, auto batch, auto wpe) {
+  const unsigned gx = (unsigned)(((int64_t)a.N + 31) / 32);
+  auto go = [&](auto tm, auto waves, auto wpe) {
     constexpr int TM = decltype(tm)::value, W = decltype(waves)::value;
-    hipLaunchKernelGGL((gemm_tokens_kernel<MODE, TM, KIND, W, decltype(batch)::value, decltype(wpe)::value>),
-                       dim3(gx, TM == 1 ? 1 : (gy < 65535u ? gy : 65535u)), dim3(64 * W), 0, s, a);
+    const unsigned gy = (unsigned)(((int64_t)a.M + 32 * TM - 1) / (32 * TM));
+    hipLaunchKernelGGL((gemm_tokens_kernel<MODE, TM, KIND, W, TM, decltype(wpe)::value>),
+                       dim3(gx, gy < 65535u ? gy : 65535u), dim3(64 * W), 0, s, a);  // row tiles loop beyond
   };
   constexpr std::integral_constant<int, 1> c1;
   constexpr std::integral_constant<int, 2> c2;
   constexpr std::integral_constant<int, 4> c4;
   constexpr std::integral_constant<int, 8> c8;
   constexpr std::integral_constant<int, 16> c16;
-  // Loads in flight come from waves or from panels per wave. One token tile: the
-  // narrow outputs of a residual product (160 workgroups at N = 5120) take 16
-  // waves of one panel (W4A4 1 x 5120 x 13824: 9.1 us, 8 waves of two 10.6), the
-  // gated pair 8 waves of one, two workgroups to a CU (1 x 13824 x 5120: 15.3 us, 4.9
-  // TB/s; three panels and one workgroup 16.6). Two token tiles, whose sums take
-  // the registers: 8 waves, two panels, but one where the residual product has
-  // several tiles of rows (64 rows: 15.4 us against 19.3, 128 rows: 29.1 against 25.4).
-  if (a.M <= 32) {
-    if constexpr (KIND == kTokResidual) go(c1, c16, c1, c4);
-    else go(c1, c8, c1, c4);
+  // Loads in flight come from many waves of one panel rather than few of several.
+  // One token tile: the narrow outputs of a residual product (160 workgroups at N =
+  // 5120) take 16 waves (W4A4 1 x 5120 x 13824: 9.1 us, 8 waves of two panels 10.6), the
+  // gated pair 8 waves, two workgroups to a CU (1 x 13824 x 5120: 15.3 us, 4.9 TB/s; three
+  // panels and one workgroup 16.6). More rows: the residual product takes a workgroup
+  // per 32 rows, which read the weight again out of the L2 (W4A8 96 x 5120 x 5120 15.8
+  // us, with two tiles per workgroup 21.4; 64 x 5120 x 13824 34.3 and 32.2), the gated pair,
+  // whose weight is the larger part, two tiles and two panels (64 x 13824 x 5120: 23.7
+  // us, four panels 42.2).
+  if constexpr (KIND == kTokResidual) {
+    if (a.M <= 32) go(c1, c16, c4);
+    else go(c1, c8, c4);
   } else {
-    if constexpr (KIND == kTokResidual) {
-      if (a.M > 64) go(c2, c8, c1, c2);
-      else go(c2, c8, c2, c2);
-    } else {
-      go(c2, c8, c2, c2);
-    }
+    if (a.M <= 32) go(c1, c8, c4);
+    else go(c2, c8, c2);
   }
   return hipGetLastError();
 }
