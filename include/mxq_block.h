@@ -151,7 +151,9 @@ int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const vo
 /* Name of the kernel that mxq_gemm_residual (gated = 0, N columns) or
  * mxq_gemm_gated (N = H, gated = 1) runs, as a static string: "pipe_..." for
  * the LDS-pipelined kernel, "tokens_..." for the split-K kernel, "invalid" for
- * another mode. Host only. */
+ * another mode. The choice goes by measured times; the environment variable
+ * MXQ_BLOCK_KERNEL=pipe or tokens, read at every call, fixes it where the
+ * pipelined kernel takes the shape. Host only. */
 const char* mxq_block_kernel_name(int mode, int gated, int mxfp4_out, int64_t M, int64_t N, int64_t K);
 
 #ifdef __cplusplus

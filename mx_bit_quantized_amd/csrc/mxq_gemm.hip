@@ -2266,8 +2266,8 @@ hipError_t launch_gemm_lowrank(const void* a_codes, const void* a_scales, const 
 // Whether the pipelined kernel is the faster one, from what both were measured to
 // take (us, one MI355X). Its workgroups take 256 x 256 outputs of the product, one
 // per CU and round; a round takes c + d per 128 elements of K, whether the tiles
-// fill the chip or not (residual, W4A4: 256 x 5120 x 5120 38 us, x 13824 84 us, 1024
-// x 5120 x 5120 40 us). 512 of the split-K kernel's 32 x 32 pieces of a residual
+// fill the chip or not (residual, W4A4: 256 x 5120 x 5120 41 us, x 13824 84 us, 1024
+// x 5120 x 5120 43 us). 512 of the split-K kernel's 32 x 32 pieces of a residual
 // product, or 256 of its 64 x 32 pairs, take a + b per 128 elements (the same shapes:
 // 18, 41 and about 70 us). W4A8 and gated figures in the same way, at K = 1024 to 13824.
 static bool pipe_pays(bool gated, int mode, int64_t M, int64_t cols, int64_t K) {
