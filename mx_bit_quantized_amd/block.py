@@ -172,6 +172,10 @@ def norm_quantize(mode, x, branch=None, gate=None, branch_scale=1.0, post_norm=N
     """
     dev = _index(x, "x")
     m, k = _matrix(x, "x")
+    if h is not None and (branch is None or not write_h):
+        raise ValueError("h is an output of a call with a branch and write_h")
+    if out_scales is not None and mode == POLICY_BF16:
+        raise ValueError("POLICY_BF16 has no out_scales")
     bf16, u8 = torch.bfloat16, torch.uint8
     px, ldx = _rows(x, "x", dev, (m, k))
     if gate is None and scale is None and shift is None:
@@ -198,10 +202,8 @@ def norm_quantize(mode, x, branch=None, gate=None, branch_scale=1.0, post_norm=N
                     ph, ldh = _rows(h, "h", dev, (m, k))
             else:
                 h = None
-        elif h is None:
-            h = x if write_h else None
-        else:
-            raise ValueError("h is an output of a call with a branch")
+        elif write_h:
+            h = x
         pos = None
         if mode == POLICY_BF16:
             if out is None:
@@ -235,7 +237,8 @@ def _operands(mode, a_codes, a_scales, w_codes, w_scales):
     dev = _index(w_codes, "w_codes")
     n, half = _matrix(w_codes, "w_codes")
     k = 2 * half
-    m = a_codes.shape[0]
+    _same(a_codes, "a_codes", dev)
+    m = _matrix(a_codes, "a_codes")[0]
     u8 = torch.uint8
     if mode == W4A8:
         pa = _ptr(a_codes, "a_codes", dev, u8, (m, k))

@@ -216,3 +216,21 @@ def test_binding_refuses_shapes_devices_and_groups():
         mxq.gemm_gated(mxq.W4A4, ac, asc, wc, wsc, mxq.GATED_SILU, bias_up=fake(64))
     with pytest.raises(ValueError, match="w_up must have shape"):
         mxq.quantize_weight_gated_mxfp4(fake(64, 64), fake(32, 64))
+
+
+def test_binding_refuses_outputs_that_the_call_does_not_write():
+    x, h = fake(6, 64), fake(6, 64)
+    with pytest.raises(ValueError, match="h is an output"):
+        mxq.norm_quantize(mxq.W4A4, x, h=h)
+    with pytest.raises(ValueError, match="h is an output"):
+        mxq.norm_quantize(mxq.W4A4, x, branch=x, h=h, write_h=False)
+    with pytest.raises(ValueError, match="no out_scales"):
+        mxq.norm_quantize(mxq.POLICY_BF16, x, out_scales=fake(1, 6, 4, dtype=torch.uint8))
+
+
+def test_binding_refuses_activations_that_are_no_matrix():
+    wc, wsc = fake(64, 32, dtype=torch.uint8), fake(1, 64, 4, dtype=torch.uint8)
+    with pytest.raises(TypeError, match="a_codes"):
+        mxq.gemm_gated(mxq.W4A4, None, None, wc, wsc, mxq.GATED_SILU)
+    with pytest.raises(ValueError, match="a_codes must be 2-D"):
+        mxq.gemm_residual(mxq.W4A4, fake(32, dtype=torch.uint8), wsc, wc, wsc, fake(1, 64))
