@@ -49,7 +49,7 @@ struct NormArgs {
   uint32_t* out_scales;
   int64_t M, ldx, ldb, ldh, ld_mod, rows_per_group, rows_per_wg;
   int K, post_norm, norm, mod_bf16;
-  float eps, branch_scale, inv_k;
+  float eps, branch_scale, k, inv_k;
 };
 
 // Sum over the 16 lanes of a DPP row, in every lane of it.
@@ -79,6 +79,16 @@ __device__ __forceinline__ uint32_t wave_max_63(uint32_t v) {
   v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));
   v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
   return v;
+}
+
+// sum / k, correctly rounded: the product with the rounded reciprocal, then one
+// step with its exact remainder (Markstein's quotient). The product alone is one
+// step off for some k (multiples of 7, 13, 41 among them), and a row of one value c
+// then keeps c 2^-24 of it, whose square competes with eps: a layer norm of 28672
+// values of 1e5 gave -0.99 in place of 0. Two operations a row.
+__device__ __forceinline__ float mean_of(float sum, float k, float inv_k) {
+  const float q = sum * inv_k;
+  return __builtin_fmaf(__builtin_fmaf(-q, k, sum), inv_k, q);
 }
 
 // 8 consecutive modulation values of a group's vector, in fp32.
@@ -175,7 +185,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(WPE))) voi
       total(mu);
       keep_packed(v);
 #pragma unroll
-      for (int i = 0; i < R; ++i) mu[i] *= a.inv_k;
+      for (int i = 0; i < R; ++i) mu[i] = mean_of(mu[i], a.k, a.inv_k);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -449,7 +459,8 @@ hipError_t launch_norm_quant(int mode, const mxq_norm_args& g, hipStream_t s) {
   a.mod_bf16 = g.mod_type == MXQ_MOD_BF16;
   a.eps = g.eps;
   a.branch_scale = g.branch_scale;
-  a.inv_k = 1.0f / (float)g.K;
+  a.k = (float)g.K;
+  a.inv_k = 1.0f / a.k;
   const int out = mode == MXQ_W4A4                   ? kOutMxfp4
                   : mode == MXQ_W4A8                 ? kOutFp8
                   : mode == MXQ_POLICY_TRANSFORM_ON  ? kOutHadamard
