@@ -19,6 +19,12 @@
  * graph, calls may overlap on one device, and results do not depend on the
  * schedule (no floating-point atomics).
  *
+ * With MXQ_CHECK_FINITE set the calls also scan their vectors (weights and
+ * biases, modulation vectors of the groups that the rows use, act_mult) before
+ * anything is written, and report values that overflowed bf16 in an output or
+ * before its quantization (by the scales, which are then past any finite
+ * block's or row's). Token scales and codes of an operand are not scanned.
+ *
  * Modulation vectors (gate, scale, shift) belong to groups of rows: a vector
  * is [groups][ld_mod], row m uses row m / rows_per_group of it (a batch item's
  * tokens, or 1 for a vector per token); rows_per_group = 0 means one group

@@ -23,6 +23,20 @@ int check_modulation(int mod_type, int64_t ld_mod, int64_t rows_per_group, int64
   return MXQ_OK;
 }
 
+// MXQ_CHECK_FINITE on a modulation vector of length n: the groups that m rows use.
+int modulation_guard(const char* what, const void* p, int mod_type, int64_t ld_mod, int64_t rows_per_group, int64_t m,
+                     int64_t n, hipStream_t stream) {
+  if (p == nullptr) return MXQ_OK;
+  const int64_t groups = rows_per_group > 0 ? (m + rows_per_group - 1) / rows_per_group : 1;
+  return mod_type == MXQ_MOD_BF16 ? finite_guard(what, p, groups, n, ld_mod, stream)
+                                  : finite_guard_f32(what, p, groups, n, ld_mod, stream);
+}
+
+// The same on a bf16 vector.
+int vector_guard(const char* what, const void* p, int64_t n, hipStream_t stream) {
+  return p == nullptr ? MXQ_OK : finite_guard(what, p, 1, n, n, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -61,10 +75,24 @@ int mxq_norm_quantize(int mode, const mxq_norm_args* args, hipStream_t stream) {
             (long long)a.M, (long long)a.K);
   if ((st = finite_guard("norm input", a.x, a.M, a.K, a.ldx, stream)) != MXQ_OK) return st;
   if (a.branch != nullptr && (st = finite_guard("branch", a.branch, a.M, a.K, a.ldb, stream)) != MXQ_OK) return st;
+  const struct { const char* what; const void* p; } vectors[] = {
+      {"post_weight", a.post_weight}, {"post_bias", a.post_bias}, {"norm weight", a.weight}, {"norm bias", a.bias}};
+  for (const auto& v : vectors)
+    if ((st = vector_guard(v.what, v.p, a.K, stream)) != MXQ_OK) return st;
+  const struct { const char* what; const void* p; } modulation[] = {{"gate", a.gate}, {"scale", a.scale}, {"shift", a.shift}};
+  for (const auto& v : modulation)
+    if ((st = modulation_guard(v.what, v.p, a.mod_type, a.ld_mod, a.rows_per_group, a.M, a.K, stream)) != MXQ_OK) return st;
+  if (mode == MXQ_POLICY_TRANSFORM_ON &&
+      (st = finite_guard_f32("transform factors", a.act_mult, 1, a.K, a.K, stream)) != MXQ_OK)
+    return st;
   st = hip_status(launch_norm_quant(mode, a, stream));
   if (st != MXQ_OK) return st;
   if (a.h != nullptr && (st = finite_guard("residual stream", a.h, a.M, a.K, a.ldh, stream)) != MXQ_OK) return st;
-  return mode == MXQ_POLICY_BF16 ? finite_guard("norm output", a.out, a.M, a.K, a.K, stream) : MXQ_OK;
+  // An h or an output that overflowed bf16 (h need not be stored: its row's norm
+  // is not finite either) leaves its mark in the scales of the quantized formats.
+  if (mode == MXQ_POLICY_BF16) return finite_guard("norm output", a.out, a.M, a.K, a.K, stream);
+  if (mode == MXQ_W4A8) return finite_guard_f32("norm output", a.out_scales, 1, a.M, a.M, stream);
+  return finite_guard_mx("norm output", a.out_scales, a.M, a.K, stream);
 }
 
 int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
@@ -88,6 +116,8 @@ int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const
     fprintf(stderr, "[mxq] gemm_residual %s M=%lld N=%lld K=%lld epi=%d kernel=%s\n", mode == MXQ_W4A4 ? "w4a4" : "w4a8",
             (long long)M, (long long)N, (long long)K, epilogue, mxq_block_kernel_name(mode, 0, 0, M, N, K));
   if ((st = finite_guard("residual", residual, M, N, N, stream)) != MXQ_OK) return st;
+  if ((st = vector_guard("bias", bias, N, stream)) != MXQ_OK) return st;
+  if ((st = modulation_guard("gate", gate, mod_type, ld_mod, rows_per_group, M, N, stream)) != MXQ_OK) return st;
   ResidualEpi e{residual, gate, ld_mod, rows_per_group, mod_type == MXQ_MOD_BF16};
   return output_guard(launch_gemm_residual(mode, a_codes, a_scales, w_codes, w_scales, bias, epilogue, e, y, M, N, K,
                                              stream),
@@ -128,10 +158,13 @@ int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const vo
     fprintf(stderr, "[mxq] gemm_gated %s%s M=%lld H=%lld K=%lld act=%d kernel=%s\n", mode == MXQ_W4A4 ? "w4a4" : "w4a8",
             y_scales != nullptr ? " -> mxfp4" : "", (long long)M, (long long)H, (long long)K, act,
             mxq_block_kernel_name(mode, 1, y_scales != nullptr, M, H, K));
+  if ((st = vector_guard("gate bias", bias_gate, H, stream)) != MXQ_OK) return st;
+  if ((st = vector_guard("up bias", bias_up, H, stream)) != MXQ_OK) return st;
   const hipError_t e = launch_gemm_gated(mode, a_codes, a_scales, w_codes, w_scales, bias_gate, bias_up, act, y,
                                            y_scales, M, H, K, stream);
-  if (y_scales != nullptr) return hip_status(e);  // MXFP4 output: always finite
-  return output_guard(e, "output", y, M, H, stream);
+  if (y_scales == nullptr) return output_guard(e, "output", y, M, H, stream);
+  if (e != hipSuccess) return MXQ_ERR_HIP;
+  return finite_guard_mx("output", y_scales, M, H, stream);
 }
 
 const char* mxq_block_kernel_name(int mode, int gated, int mxfp4_out, int64_t M, int64_t N, int64_t K) {

@@ -33,16 +33,38 @@ inline int check_mk(int64_t rows, int64_t K, int64_t ld) {
 
 inline int hip_status(hipError_t e) { return e == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
 
+// The guard's status for a scan's result.
+inline int guard_status(int scan_error, bool bad, const char* what, int64_t rows, int64_t cols) {
+  if (scan_error != 0) return MXQ_ERR_HIP;
+  if (!bad) return MXQ_OK;
+  if (log_enabled()) fprintf(stderr, "[mxq] non-finite value in %s [%lld x %lld]\n", what, (long long)rows,
+                             (long long)cols);
+  return MXQ_ERR_NONFINITE;
+}
+
 // MXQ_CHECK_FINITE: scan a bf16 [rows][ld] input (or output) for infinities and
 // NaNs; MXQ_OK when the guard is off.
 inline int finite_guard(const char* what, const void* x, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream) {
   if (!check_finite_enabled()) return MXQ_OK;
   bool bad = false;
-  if (scan_nonfinite_bf16(x, rows, cols, ld, stream, &bad) != 0) return MXQ_ERR_HIP;
-  if (!bad) return MXQ_OK;
-  if (log_enabled()) fprintf(stderr, "[mxq] non-finite value in %s [%lld x %lld]\n", what, (long long)rows,
-                             (long long)cols);
-  return MXQ_ERR_NONFINITE;
+  const int err = scan_nonfinite_bf16(x, rows, cols, ld, stream, &bad);
+  return guard_status(err, bad, what, rows, cols);
+}
+
+// The same of a float32 [rows][ld] operand.
+inline int finite_guard_f32(const char* what, const void* x, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream) {
+  if (!check_finite_enabled()) return MXQ_OK;
+  bool bad = false;
+  const int err = scan_nonfinite_f32(x, rows, cols, ld, stream, &bad);
+  return guard_status(err, bad, what, rows, cols);
+}
+
+// The same of the scales of an MXFP4 output: blocks quantized from an infinity or a NaN.
+inline int finite_guard_mx(const char* what, const void* scales, int64_t rows, int64_t cols, hipStream_t stream) {
+  if (!check_finite_enabled()) return MXQ_OK;
+  bool bad = false;
+  const int err = scan_nonfinite_mx(scales, rows, cols, stream, &bad);
+  return guard_status(err, bad, what, rows, cols);
 }
 
 // a launch's status, then the guard on its bf16 output

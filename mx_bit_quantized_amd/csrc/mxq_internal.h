@@ -134,6 +134,10 @@ hipError_t launch_mxfp4_layout(bool to_canonical, const void* src_codes, const v
 // error).
 bool check_finite_enabled();
 int scan_nonfinite_bf16(const void* x, int64_t rows, int64_t cols, int64_t ld, hipStream_t s, bool* found);
+// The same of a float32 matrix, and of MXFP4 scales [ceil(cols/128)][rows][4]
+// (a block that held an infinity or a NaN when it was quantized).
+int scan_nonfinite_f32(const void* x, int64_t rows, int64_t cols, int64_t ld, hipStream_t s, bool* found);
+int scan_nonfinite_mx(const void* scales, int64_t rows, int64_t cols, hipStream_t s, bool* found);
 
 // Name of the GEMM kernel variant launch_gemm picks for a shape (for logs).
 const char* gemm_variant_name(int mode, int64_t M, int64_t N, int64_t K);
