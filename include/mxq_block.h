@@ -115,7 +115,10 @@ int mxq_norm_quantize(int mode, const mxq_norm_args* args, hipStream_t stream);
  *   y         device bf16 [M][N] (output); may be residual itself
  * Any M and N, K a multiple of 32. Rows in the tens run a kernel that splits
  * K over a workgroup's waves; its sums are taken in another order than
- * mxq_gemm's.
+ * mxq_gemm's. So do, at any M and then far slower than the pipelined kernel, N
+ * below 256 or no multiple of 8, K below 512 (W4A8: 384), codes of 2 GiB or more,
+ * and a gate of several groups (rows_per_group > 0) whose ld_mod is no multiple
+ * of 8.
  */
 int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
                       const void* bias, int epilogue, const void* residual, const void* gate, int mod_type,
@@ -159,7 +162,9 @@ int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const vo
  * the LDS-pipelined kernel, "tokens_..." for the split-K kernel, "invalid" for
  * another mode. The choice goes by measured times; the environment variable
  * MXQ_BLOCK_KERNEL=pipe or tokens, read at every call, fixes it where the
- * pipelined kernel takes the shape. Host only. */
+ * pipelined kernel takes the shape. The name goes by the shape: a residual
+ * product whose gate has several groups (rows_per_group > 0) with ld_mod no
+ * multiple of 8 runs the split-K kernel at any size. Host only. */
 const char* mxq_block_kernel_name(int mode, int gated, int mxfp4_out, int64_t M, int64_t N, int64_t K);
 
 #ifdef __cplusplus

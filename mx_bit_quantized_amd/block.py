@@ -338,5 +338,8 @@ def gemm_gated(mode, a_codes, a_scales, w_codes, w_scales, act, bias_gate=None, 
 
 
 def block_kernel_name(mode, M, N, K, gated=False, mxfp4_out=False):
-    """Name of the kernel that gemm_residual (or with ``gated`` gemm_gated, N = H) runs for a shape (host query)."""
+    """Name of the kernel that gemm_residual (or with ``gated`` gemm_gated, N = H) runs for a shape (host query).
+
+    By the shape alone: gemm_residual with a gate of several groups whose row stride is no multiple of 8 runs the split-K one.
+    """
     return _lib().mxq_block_kernel_name(int(mode), int(gated), int(mxfp4_out), int(M), int(N), int(K)).decode()

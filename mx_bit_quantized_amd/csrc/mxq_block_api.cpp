@@ -37,6 +37,11 @@ int vector_guard(const char* what, const void* p, int64_t n, hipStream_t stream)
   return p == nullptr ? MXQ_OK : finite_guard(what, p, 1, n, n, stream);
 }
 
+const char* kernel_name(int mode, bool pipelined) {
+  if (pipelined) return mode == MXQ_W4A4 ? "pipe_w4a4" : "pipe_w4a8";
+  return mode == MXQ_W4A4 ? "tokens_w4a4" : "tokens_w4a8";
+}
+
 }  // namespace
 
 extern "C" {
@@ -112,13 +117,13 @@ int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
       !aligned16_or_null(bias) || !aligned16(residual) || !aligned16_or_null(gate) || !aligned16(y))
     return MXQ_ERR_ALIGN;
+  const ResidualEpi e{residual, gate, ld_mod, rows_per_group, mod_type == MXQ_MOD_BF16};
   if (log_enabled())
     fprintf(stderr, "[mxq] gemm_residual %s M=%lld N=%lld K=%lld epi=%d kernel=%s\n", mode == MXQ_W4A4 ? "w4a4" : "w4a8",
-            (long long)M, (long long)N, (long long)K, epilogue, mxq_block_kernel_name(mode, 0, 0, M, N, K));
+            (long long)M, (long long)N, (long long)K, epilogue, kernel_name(mode, gemm_residual_pipelined(mode, M, N, K, e)));
   if ((st = finite_guard("residual", residual, M, N, N, stream)) != MXQ_OK) return st;
   if ((st = vector_guard("bias", bias, N, stream)) != MXQ_OK) return st;
   if ((st = modulation_guard("gate", gate, mod_type, ld_mod, rows_per_group, M, N, stream)) != MXQ_OK) return st;
-  ResidualEpi e{residual, gate, ld_mod, rows_per_group, mod_type == MXQ_MOD_BF16};
   return output_guard(launch_gemm_residual(mode, a_codes, a_scales, w_codes, w_scales, bias, epilogue, e, y, M, N, K,
                                              stream),
                       "output", y, M, N, stream);
@@ -169,10 +174,8 @@ int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const vo
 
 const char* mxq_block_kernel_name(int mode, int gated, int mxfp4_out, int64_t M, int64_t N, int64_t K) {
   if (mode != MXQ_W4A4 && mode != MXQ_W4A8) return "invalid";
-  const bool pipe = gated ? gemm_gated_pipelined(mode, M, N, K, mxfp4_out != 0)
-                          : gemm_residual_pipelined(mode, M, N, K, ResidualEpi{});
-  if (pipe) return mode == MXQ_W4A4 ? "pipe_w4a4" : "pipe_w4a8";
-  return mode == MXQ_W4A4 ? "tokens_w4a4" : "tokens_w4a8";
+  return kernel_name(mode, gated ? gemm_gated_pipelined(mode, M, N, K, mxfp4_out != 0)
+                                 : gemm_residual_pipelined(mode, M, N, K, ResidualEpi{}));
 }
 
 }  // extern "C"
