@@ -72,12 +72,14 @@ enum { MXQ_GATED_SILU = 0, MXQ_GATED_GELU_TANH = 1 };
  *   norm        MXQ_NORM_RMS or _LAYER; weight, bias: device bf16 [K] or null
  *   scale,shift modulation vectors or null (zeros)
  *   eps         positive and finite, for both norms
- *   act_mult    device float32 [K]: MXQ_POLICY_TRANSFORM_ON only (K % 128 == 0)
+ *   act_mult    device float32 [K]: MXQ_POLICY_TRANSFORM_ON only (K % 128 == 0),
+ *               null in the other modes
  *   h           device bf16 [M][ldh] (output) or null; may be x or branch
  *               itself (same pointer and stride), else may not overlap an input
  *   out         device: bf16 [M][K], or codes; out_scales: scales (null for bf16)
  *   M, K        K a multiple of 32, at most MXQ_NORM_MAX_K (MXQ_ERR_SHAPE)
  * gate, post_norm, branch_scale != 1 or h without a branch: MXQ_ERR_NULL.
+ * act_mult or out_scales in a mode that does not take them: MXQ_ERR_MODE.
  * Values whose squares sum past fp32's range (|v| about 1e18) are not finite
  * inputs of a norm.
  */

@@ -75,6 +75,9 @@ int mxq_norm_quantize(int mode, const mxq_norm_args* args, hipStream_t stream) {
   if (a.ldx % 8 != 0 || (a.branch != nullptr && a.ldb % 8 != 0) || (a.h != nullptr && a.ldh % 8 != 0) ||
       (modulated && a.ld_mod % 8 != 0))
     return MXQ_ERR_ALIGN;
+  // operands that the mode does not read
+  if ((a.act_mult != nullptr && mode != MXQ_POLICY_TRANSFORM_ON) || (a.out_scales != nullptr && mode == MXQ_POLICY_BF16))
+    return MXQ_ERR_MODE;
   if (log_enabled())
     fprintf(stderr, "[mxq] norm_quantize mode=%d norm=%d post=%d M=%lld K=%lld\n", mode, a.norm, a.post_norm,
             (long long)a.M, (long long)a.K);
