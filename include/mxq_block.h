@@ -115,7 +115,7 @@ int mxq_norm_quantize(int mode, const mxq_norm_args* args, hipStream_t stream);
  *   gate      modulation vector [groups][ld_mod >= N] of mod_type, or null
  *             (ones; ld_mod, rows_per_group and mod_type are then not read)
  *   y         device bf16 [M][N] (output); may be residual itself
- * Any M and N, K a multiple of 32. Rows in the tens run a kernel that splits
+ * Any M, N at most 2^28 - 32, K a multiple of 32. Rows in the tens run a kernel that splits
  * K over a workgroup's waves; its sums are taken in another order than
  * mxq_gemm's. So do, at any M and then far slower than the pipelined kernel, N
  * below 256 or no multiple of 8, K below 512 (W4A8: 384), codes of 2 GiB or more,
@@ -153,7 +153,7 @@ int mxq_quantize_weight_gated_mxfp4(const void* w_gate, const void* w_up, int64_
  *                     of the second projection (M * H/2 code bytes in panels,
  *                     scales [ceil(H/128)][M][4]): the codes of
  *                     mxq_quantize_act(MXQ_W4A4, the bf16 hidden state)
- * H and K multiples of 32, any M.
+ * H and K multiples of 32, H at most 2^28 - 32, any M.
  */
 int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
                    const void* bias_gate, const void* bias_up, int act, void* y, void* y_scales, int64_t M, int64_t H,

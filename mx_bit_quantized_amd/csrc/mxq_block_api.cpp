@@ -111,7 +111,7 @@ int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const
   if (epilogue != MXQ_EPI_NONE && epilogue != MXQ_EPI_GELU_TANH) return MXQ_ERR_MODE;
   int st = check_mk(M, K, K);
   if (st != MXQ_OK) return st;
-  if (N < 0 || N >= kMaxDim) return MXQ_ERR_SHAPE;
+  if (N < 0 || N > kMaxBlockCols) return MXQ_ERR_SHAPE;
   if (gate != nullptr && (st = check_modulation(mod_type, ld_mod, rows_per_group, N)) != MXQ_OK) return st;
   if (M == 0 || N == 0) return MXQ_OK;
   if (a_codes == nullptr || a_scales == nullptr || w_codes == nullptr || w_scales == nullptr || residual == nullptr ||
@@ -155,7 +155,7 @@ int mxq_gemm_gated(int mode, const void* a_codes, const void* a_scales, const vo
   if (y_scales != nullptr && mode != MXQ_W4A4) return MXQ_ERR_MODE;
   int st = check_mk(M, K, K);
   if (st != MXQ_OK) return st;
-  if (H < 0 || H >= kMaxDim / 2 || H % 32 != 0) return MXQ_ERR_SHAPE;
+  if (H < 0 || H > kMaxBlockCols || H % 32 != 0) return MXQ_ERR_SHAPE;
   if (M == 0 || H == 0) return MXQ_OK;
   if (a_codes == nullptr || a_scales == nullptr || w_codes == nullptr || w_scales == nullptr || y == nullptr)
     return MXQ_ERR_NULL;

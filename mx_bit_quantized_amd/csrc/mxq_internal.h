@@ -101,6 +101,11 @@ struct ResidualEpi {
   int mod_bf16;
 };
 
+// Most output columns of the products: the split-K kernel has a workgroup of 512
+// threads (up to 2^27 columns, where it pays, 1024) per 32 of them, and a grid
+// holds less than 2^32 threads.
+constexpr int64_t kMaxBlockCols = (int64_t(1) << 28) - 32;
+
 // Few rows, and shapes outside the pipelined kernel's (mode 0 = W4A4, 1 = W4A8).
 hipError_t launch_tokens_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes,
                                   const void* w_scales, const void* bias, int epilogue, const ResidualEpi& e, void* y,

@@ -291,7 +291,7 @@ static hipError_t launch_tokens_kind(const TokArgs& a, hipStream_t s) {
   // whose weight is the larger part, two tiles and two panels (64 x 13824 x 5120: 23.7
   // us, four panels 42.2).
   if constexpr (KIND == kTokResidual) {
-    if (a.M <= 32) go(c1, c16, c4);
+    if (a.M <= 32 && gx < (1u << 22)) go(c1, c16, c4);  // (a grid's threads: kMaxBlockCols)
     else go(c1, c8, c4);
   } else {
     if (a.M <= 32) go(c1, c8, c4);
