@@ -76,7 +76,9 @@ enum { MXQ_GATED_SILU = 0, MXQ_GATED_GELU_TANH = 1 };
  *               null in the other modes
  *   h           device bf16 [M][ldh] (output) or null; may be x or branch
  *               itself (same pointer and stride), else may not overlap an input
- *   out         device: bf16 [M][K], or codes; out_scales: scales (null for bf16)
+ *   out         device: bf16 [M][K], or codes; out_scales: scales (null for
+ *               bf16). A bf16 out may be x or branch itself where those are
+ *               dense; else outputs may not overlap an input or each other
  *   M, K        K a multiple of 32, at most MXQ_NORM_MAX_K (MXQ_ERR_SHAPE)
  * gate, post_norm, branch_scale != 1 or h without a branch: MXQ_ERR_NULL.
  * act_mult or out_scales in a mode that does not take them: MXQ_ERR_MODE.
@@ -114,13 +116,14 @@ int mxq_norm_quantize(int mode, const mxq_norm_args* args, hipStream_t stream);
  *   residual  device bf16 [M][N] (dense)
  *   gate      modulation vector [groups][ld_mod >= N] of mod_type, or null
  *             (ones; ld_mod, rows_per_group and mod_type are then not read)
- *   y         device bf16 [M][N] (output); may be residual itself
- * Any M, N at most 2^28 - 32, K a multiple of 32. Rows in the tens run a kernel that splits
- * K over a workgroup's waves; its sums are taken in another order than
- * mxq_gemm's. So do, at any M and then far slower than the pipelined kernel, N
- * below 256 or no multiple of 8, K below 512 (W4A8: 384), codes of 2 GiB or more,
- * and a gate of several groups (rows_per_group > 0) whose ld_mod is no multiple
- * of 8.
+ *   y         device bf16 [M][N] (output); may be residual itself, else may not
+ *             overlap an input
+ * Any M, N at most 2^28 - 32, K a multiple of 32. Rows in the tens run a kernel
+ * that splits K over a workgroup's waves; its sums are taken in another order
+ * than mxq_gemm's. So do, at any M and then far slower than the pipelined
+ * kernel, N below 256 or no multiple of 8, K below 512 (W4A8: 384), codes of 2
+ * GiB or more, and a gate of several groups (rows_per_group > 0) whose ld_mod is
+ * no multiple of 8.
  */
 int mxq_gemm_residual(int mode, const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
                       const void* bias, int epilogue, const void* residual, const void* gate, int mod_type,
