@@ -584,9 +584,14 @@ struct FuseArgs {
 // a tile's code stages come four residual stages: token rows 32 q .. 32 q + 31 of
 // the tile's upper half (the wm = 0 waves') ride in the W role of stage q, those of
 // its lower half (wm = 1) in the X role, 512 bytes a row, so the copies run ahead
-// through the ring like any others and no load waits in the epilogue, where its
-// wait would also drain the copies in flight (vmcnt counts them in order). The
-// residual stages are the tile's epilogue: in stage q each wave finishes, rounds
+// through the ring like any others and no load of a residual waits in the epilogue,
+// where its wait would also drain the copies in flight (vmcnt counts them in
+// order). The forms with a bias do not reach that: the gate's kind (none, bf16,
+// fp32) is decided at run time, both kinds' addresses stay live, and 10 to 15
+// registers spill, whose 10 to 15 reloads a stage wait for vmcnt 0, as do the loads of
+// a gate vector per row. W4A4 32760 x 5120 x 13824 with a bias: 1140 us without a gate,
+// 1190 with an fp32 one, 1279 with one per row (bf16: 1200); W4A8 1570, 1652, 1732
+// (1652). The residual stages are the tile's epilogue: in stage q each wave finishes, rounds
 // and stores its row group j = q, and the next tile's first stage carries none.
 // (With the sums finished in place and left to the ordinary epilogue, the
 // accumulators went through the vector unit twice: W4A4 32760 x 5120 x 5120 took
@@ -2264,8 +2269,8 @@ hipError_t launch_gemm_lowrank(const void* a_codes, const void* a_scales, const 
 // ---- the operators around the product (FUSE)
 
 // Whether the pipelined kernel is the faster one, from what both were measured to
-// take (us, one MI355X). Its workgroups take 256 x 256 outputs of the product, one
-// per CU and round; a round takes c + d per 128 elements of K, whether the tiles
+// take (us, one MI355X with 256 CUs). Its workgroups take 256 x 256 outputs of the
+// product, one per CU and round; a round takes c + d per 128 elements of K, whether the tiles
 // fill the chip or not (residual, W4A4: 256 x 5120 x 5120 41 us, x 13824 84 us, 1024
 // x 5120 x 5120 43 us). 512 of the split-K kernel's 32 x 32 pieces of a residual
 // product, or 256 of its 64 x 32 pairs, take a + b per 128 elements (the same shapes:

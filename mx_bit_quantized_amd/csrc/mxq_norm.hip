@@ -16,11 +16,19 @@
 // rows at a time, so that the per-channel factors A, B, g (fp32, up to 10x a
 // row's bytes) are read and combined once per workgroup, not once per row: a
 // wave per row, which needs no barrier, would pull them through the L2 for
-// every row. Workgroups take contiguous runs of rows, those of one XCD
-// adjacent, so that the 64-byte pieces of a code panel's lines meet in one L2.
+// every row. Workgroups take contiguous runs of rows. Where their number is a
+// multiple of 8, the runs of one XCD are adjacent, so that the 64-byte pieces of a
+// code panel's lines meet in one L2; other grids, the 511 workgroups of 75600 x
+// 5120 too, keep the launch's order.
 // 75600 x 5120, layer norm with gate and modulation: 628 us in bf16 (4.93 TB/s
-// over x, branch, h and out; a 2 GiB copy reaches 4.92), MXFP4 544 us (4.65), FP8
-// 601 us (4.51, three reductions a row). One row of 5120: 3.0 - 4.4 us.
+// over x, branch, h and out; a 2 GiB copy reaches 4.92), MXFP4 543 us (4.65), FP8
+// 603 us (4.49, three reductions a row), transformed MXFP4 835 us (3.03: the
+// transform's arithmetic and lane exchanges come on top). A vector per token, 18900
+// x 5120: 400 us with fp32 vectors and 285 us with bf16 ones, 4.84 and 4.75 TB/s with
+// the vectors' bytes. One row of 5120: 2.7 - 4.3 us.
+// Spills: from K = 8193 on with a post-norm to MXFP4 (8 registers, transformed 16),
+// past 16384 in every form but FP8 (20 to 72): 4000 x 28672 takes 103 us as a plain
+// RMS norm, 223 us with a branch and its norm and 305 us to MXFP4.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

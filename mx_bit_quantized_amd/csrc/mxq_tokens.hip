@@ -8,8 +8,10 @@
 // gate rows and 32 up rows of the same hidden columns, adjacent in the packed
 // weight) and its waves (8 or 16) split K: wave w of W takes the 128-element code panels
 // w, w + W, ... A wave's load of a panel's 32 rows is 2 KiB of consecutive
-// memory, kBatch panels are in flight per wave, and nothing goes through LDS on
-// the way to the matrix cores: no row is shared between waves. The tokens are
+// memory. It loads BATCH panels (one, or two with two token tiles), waits and
+// multiplies, so that what overlaps loads with arithmetic is the other waves.
+// Nothing goes through LDS on the way to the matrix cores: no row is shared
+// between waves. The tokens are
 // the MFMA's second operand, 32 at a time, from L2; rows past M repeat the last
 // one (their columns are not written). The waves' partial sums meet in LDS,
 // in wave order, so a result depends on the shape only.
@@ -90,7 +92,8 @@ struct TokArgs {
   int mod_bf16, act;
 };
 
-// TM: 32-token tiles per workgroup, which share each load of the weight.
+// TM: 32-token tiles per workgroup, which share each load of the weight. BATCH:
+// panels that a wave has in flight.
 template <int MODE, int TM, int KIND, int WAVES, int BATCH, int WPE>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WPE))) void gemm_tokens_kernel(const TokArgs a) {
   constexpr bool GATED = KIND != kTokResidual;
@@ -284,12 +287,15 @@ static hipError_t launch_tokens_kind(const TokArgs& a, hipStream_t s) {
   // Loads in flight come from many waves of one panel rather than few of several.
   // One token tile: the narrow outputs of a residual product (160 workgroups at N =
   // 5120) take 16 waves (W4A4 1 x 5120 x 13824: 9.1 us, 8 waves of two panels 10.6), the
-  // gated pair 8 waves, two workgroups to a CU (1 x 13824 x 5120: 15.3 us, 4.9 TB/s; three
-  // panels and one workgroup 16.6). More rows: the residual product takes a workgroup
-  // per 32 rows, which read the weight again out of the L2 (W4A8 96 x 5120 x 5120 15.8
-  // us, with two tiles per workgroup 21.4; 64 x 5120 x 13824 34.3 and 32.2), the gated pair,
-  // whose weight is the larger part, two tiles and two panels (64 x 13824 x 5120: 23.7
-  // us, four panels 42.2).
+  // gated pair 8 waves, two workgroups to a CU (1 x 13824 x 5120: 15.3 us, three panels
+  // and one workgroup 16.6, measured side by side). With three sets of weights in
+  // turn, which the Infinity Cache holds, the two products take
+  // 8.6 and 13.5 us now, from HBM (24 and 16 sets) 11.3 us (3.3 TB/s) and 17.1 us (4.4).
+  // More rows: the residual product takes a workgroup per 32 rows, which read the
+  // weight again out of the L2 (W4A8 96 x 5120 x 5120 15.8 us, with two tiles per
+  // workgroup 21.4; 64 x 5120 x 13824 34.3 and 32.2), the gated pair, whose weight is
+  // the larger part, two tiles and two panels (64 x 13824 x 5120: 23.7 us, four
+  // panels 42.2).
   if constexpr (KIND == kTokResidual) {
     if (a.M <= 32 && gx < (1u << 22)) go(c1, c16, c4);  // (a grid's threads: kMaxBlockCols)
     else go(c1, c8, c4);
