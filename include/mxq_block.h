@@ -83,7 +83,8 @@ enum { MXQ_GATED_SILU = 0, MXQ_GATED_GELU_TANH = 1 };
  * gate, post_norm, branch_scale != 1 or h without a branch: MXQ_ERR_NULL.
  * act_mult or out_scales in a mode that does not take them: MXQ_ERR_MODE.
  * Values whose squares sum past fp32's range (|v| about 1e18) are not finite
- * inputs of a norm.
+ * inputs of a norm: the row's output is NaN (and its h, for the branch's norm),
+ * which MXQ_CHECK_FINITE reports.
  */
 typedef struct mxq_norm_args {
   const void* x;

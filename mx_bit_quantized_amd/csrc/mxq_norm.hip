@@ -213,7 +213,12 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(WPE))) voi
     total(rs);
     keep_packed(v);
 #pragma unroll
-    for (int i = 0; i < R; ++i) rs[i] = 1.0f / __builtin_sqrtf(__builtin_fmaf(rs[i], a.inv_k, a.eps));
+    for (int i = 0; i < R; ++i) {
+      // (a sum past fp32's range is no norm: 0 times its infinity makes the row NaN,
+      // where 1 / sqrt(infinity) = 0 would leave finite values, the bias)
+      const float v = __builtin_fmaf(rs[i], a.inv_k, a.eps);
+      rs[i] = __builtin_fmaf(v, 0.0f, 1.0f / __builtin_sqrtf(v));
+    }
   };
 
   // the factors of one chunk: gate side (GW, GB), then norm side (A, B)
