@@ -18,7 +18,8 @@ Names mirror the C ABI without its ``mxq_`` prefix:
     qlinear_noalloc(policy, expert, block, x, w_codes, w_scales, y, bias=None, epilogue=EPI_NONE)
 
 The operators around the linears (include/mxq_block.h: norm_quantize, gemm_residual, gemm_gated)
-are in block.py and offered here under the same names.
+are in block.py, those of the attention half of a block (include/mxq_attention.h: page_plan, rotary_qkv,
+attention, attention_paged) in attn.py; all are offered here under the same names.
 """
 
 import ctypes
@@ -674,13 +675,20 @@ def lowrank_up(y_pre, t, l2, epilogue=EPI_NONE, y=None, stream=None):
 
 _BLOCK = ("GATED_GELU_TANH", "GATED_SILU", "NORM_LAYER", "NORM_MAX_K", "NORM_NONE", "NORM_RMS", "block_kernel_name",
           "gemm_gated", "gemm_residual", "norm_quantize", "quantize_weight_gated_mxfp4")
+_ATTN = ("KV_BF16", "KV_MXFP8", "MAX_REQUESTS", "ROTARY_NORM_HEAD", "ROTARY_NORM_NONE", "ROTARY_NORM_ROW", "KvCache",
+              "PagePlan", "attention", "attention_paged", "kv_cache", "page_plan", "rotary_frequencies", "rotary_qkv")
 
 
 def __getattr__(name):
-    """Names of block.py, which imports torch: bound here at their first use."""
-    if name not in _BLOCK:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import block
+    """Names of block.py and attn.py, which import torch: bound here at their first use."""
+    if name in _BLOCK:
+        from . import block
 
-    globals().update({n: getattr(block, n) for n in _BLOCK})
+        globals().update({n: getattr(block, n) for n in _BLOCK})
+    elif name in _ATTN:
+        from . import attn
+
+        globals().update({n: getattr(attn, n) for n in _ATTN})
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     return globals()[name]

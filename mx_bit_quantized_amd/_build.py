@@ -26,7 +26,8 @@ ARCH = "gfx950"
 
 DEVICE_SOURCES = ["mxq_api.cpp", "mxq_quant.hip", "mxq_gemm.hip", "mxq_select.hip", "mxq_lowrank.hip",
                   "mxq_layout.hip", "mxq_noalloc.hip", "mxq_check.hip", "mxq_block_api.cpp", "mxq_norm.hip",
-                  "mxq_tokens.hip"]
+                  "mxq_tokens.hip", "mxq_attention_api.cpp", "mxq_pages.hip", "mxq_rotary.hip", "mxq_attention.hip",
+                  "mxq_paged.hip"]
 
 COMMON_FLAGS = [
     "-O3",

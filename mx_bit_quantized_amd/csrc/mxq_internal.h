@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mxq_attention.h"
 #include "mxq_block.h"
 
 namespace mxq {
@@ -127,6 +128,18 @@ hipError_t launch_gemm_gated(int mode, const void* a_codes, const void* a_scales
 // Weight packing of a gated block's two projections, rows interleaved by 32.
 hipError_t launch_mxfp4_quant_gated(const void* w_gate, const void* w_up, int64_t H, int64_t K, int64_t ld, void* codes,
                                     void* scales, hipStream_t s);
+
+// The attention half of a block (include/mxq_attention.h).
+hipError_t launch_page_plan(const int32_t* cached, const int32_t* added, int32_t* block_table, const int32_t* free_pages,
+                            int64_t requests, int64_t width, int64_t n_free, int64_t page_size, int64_t tokens,
+                            int32_t* slots, int32_t* positions, int32_t* starts, int32_t* lengths, int32_t* taken,
+                            hipStream_t s);
+hipError_t launch_rotary_qkv(const mxq_rotary_args& args, const mxq_kv_cache* cache, hipStream_t s);
+bool attention_fits(const mxq_attention_args& args);     // in one grid
+size_t attention_workspace(const mxq_attention_args& args);
+hipError_t launch_attention(const mxq_attention_args& args, void* workspace, hipStream_t s);
+size_t paged_workspace(const mxq_paged_args& args, const mxq_kv_cache& cache);
+hipError_t launch_attention_paged(const mxq_paged_args& args, const mxq_kv_cache& cache, void* workspace, hipStream_t s);
 
 // MXFP4 codes and scales between the library layout (code panels, group-major
 // scales) and the canonical row-major one ([rows][K/2], [rows][K/32]).

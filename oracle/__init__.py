@@ -25,6 +25,8 @@ quantize-dequantize emulation):
 * ``select``   - calibration-driven block selection: block-replay SQNR (OFF
                  = plain MXFP4, ON = transform) and the tiered rule ladder that
                  emits the policy artifact.
+* ``attention`` - the attention half of a block: page plan, RMS norm and rotary
+                 positions, MXFP8 blocks, attention with windows and sinks.
 * ``linear``   - dequantize-then-fp64 matmul (the QDQ result), tanh-GELU, the
                  per-block policy lookup and the output tolerance check.
 
@@ -81,6 +83,15 @@ from .select import (
     select_mode,
     select_policy,
     block_replay_sums,
+)
+from .attention import (
+    attention_rows,
+    mxfp8_dequantize,
+    mxfp8_quantize,
+    page_plan,
+    rms_norm,
+    rotate,
+    visible,
 )
 from .linear import (
     W4A4,
