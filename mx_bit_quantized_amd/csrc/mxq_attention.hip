@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "mxq_attention.h"
 #include "mxq_convert.h"
 #include "mxq_device.h"
@@ -30,6 +32,19 @@ typedef unsigned u32x2_v __attribute__((ext_vector_type(2)));
 
 constexpr int kKeys = 64;  // keys of a tile
 
+// n / d for n < 2^31 as a product: mul = ceil(2^(32 + shift) / d), 2^shift < d <= 2^(shift + 1).
+struct Divider {
+  uint32_t mul, shift, d;
+};
+static Divider divider(uint32_t d) {
+  if (d == 1) return {0, 0, 1};
+  const uint32_t shift = 31 - __builtin_clz(d - 1);
+  return {(uint32_t)(((uint64_t(1) << (32 + shift)) + d - 1) / d), shift, d};
+}
+__device__ __forceinline__ int divide(int n, const Divider& by) {
+  return by.d == 1 ? n : (int)(__umulhi((uint32_t)n, by.mul) >> by.shift);
+}
+
 struct AttnArgs {
   const uint16_t* q;
   const uint16_t* k;
@@ -40,14 +55,9 @@ struct AttnArgs {
   float* part;
   int64_t ldq, ldk, ldv, ldo;
   int sequences, Mq, Mk, left, right, sinks, kv_heads, group, slots, items, splits;
-  float scale_log2;
+  Divider by_group, by_slots, by_splits;
+  float scale_log2, slack;  // slack: how far a score may lie above the running maximum
 };
-
-// A copy of 16 bytes a lane from memory to LDS: lane i's lands at lds + 16 i.
-__device__ __forceinline__ void copy16(const void* src, void* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
-}
 
 __device__ __forceinline__ float other_half_max(float v) {
   const u32x2_v r = __builtin_amdgcn_permlane32_swap(as_uint(v), as_uint(v), false, false);
@@ -70,205 +80,417 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
   return D == 128 ? c ^ ((row & 3) << 2) : c ^ (((row >> 1) & 1) << 2);
 }
 
-template <int D, int QT, int NW>
-__global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs a) {
-  constexpr int ROWS = 32 * QT * NW, CH = D / 8, TILE = kKeys * D * 2;
-  constexpr int COPIES = TILE / 1024 / NW;  // of 1 KiB, per wave and tensor
-  extern __shared__ __attribute__((aligned(128))) uint8_t lds[];  // K, V of one tile, K, V of the next
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, l32 = lane & 31;
+// What a workgroup works on: a tile of rows of one sequence and key head, and the key
+// tiles that its queries see.
+struct Work {
+  int hk, split, q0, k0, nq, nk;
+  int row0, rows;  // of queries and heads (below 2^31)
+  int tbeg, nsink, t_first, t_last;
+};
 
-  // work item: XCDs take runs of neighbouring items (tiles of one key head meet in one L2)
+template <int ROWS>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int lane, Work& w) {
+  // XCDs take runs of neighbouring items (tiles of one key head meet in one L2)
   const int per_xcd = (a.items + 7) >> 3;
   const int lin = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per_xcd || lin >= a.items) return;
-  const int split = lin % a.splits, item = lin / a.splits;
-  const int hk = item / a.slots, slot = a.slots - 1 - item % a.slots;
+  if ((int)(blockIdx.x >> 3) >= per_xcd || lin >= a.items) return false;
+  const int item = divide(lin, a.by_splits);
+  w.split = lin - item * a.splits;
+  w.hk = divide(item, a.by_slots);
+  const int slot = a.slots - 1 - (item - w.hk * a.slots);
 
   // the sequence and tile of a slot: sequence b owns the slots from
   // floor(starts_q[b] G / ROWS) + b on, enough of them for its rows
-  int b = 0, q0 = 0, nq = a.Mq, k0 = 0, nk = a.Mk, tile = slot;
+  w.q0 = 0; w.nq = a.Mq; w.k0 = 0; w.nk = a.Mk;
+  int tile = slot;
   if (a.starts_q != nullptr) {
     int lo = 0, hi = a.sequences;  // first slot of lo <= slot < that of hi
     while (hi - lo > 1) {
       const int step = (hi - lo + 63) >> 6, probe = lo + lane * step;
       const bool in = probe < hi;
-      const int64_t s = in ? min(max(a.starts_q[probe], 0), a.Mq) : 0;
+      const int s = in ? min(max(a.starts_q[probe], 0), a.Mq) : 0;
       const uint64_t ok = __ballot(in && (lane == 0 || s * a.group / ROWS + probe <= slot));
       const int last = 63 - __builtin_clzll(ok | 1);
       hi = min(hi, lo + (last + 1) * step);
       lo += last * step;
     }
-    b = __builtin_amdgcn_readfirstlane(lo);
-    q0 = min(max(a.starts_q[b], 0), a.Mq);
-    nq = min(max(a.starts_q[b + 1], q0), a.Mq) - q0;
-    k0 = min(max(a.starts_k[b], 0), a.Mk);
-    nk = min(max(a.starts_k[b + 1], k0), a.Mk) - k0;
-    tile = slot - (int)((int64_t)q0 * a.group / ROWS) - b;
+    const int b = __builtin_amdgcn_readfirstlane(lo);
+    w.q0 = min(max(a.starts_q[b], 0), a.Mq);
+    w.nq = min(max(a.starts_q[b + 1], w.q0), a.Mq) - w.q0;
+    w.k0 = min(max(a.starts_k[b], 0), a.Mk);
+    w.nk = min(max(a.starts_k[b + 1], w.k0), a.Mk) - w.k0;
+    tile = slot - w.q0 * a.group / ROWS - b;
   }
-  const int64_t rows = (int64_t)nq * a.group;
-  const int64_t row0 = (int64_t)tile * ROWS;
-  if (tile < 0 || row0 >= rows) return;
+  w.rows = w.nq * a.group;
+  if (tile < 0 || tile > (w.rows - 1) / ROWS || w.rows == 0) return false;
+  w.row0 = tile * ROWS;
 
-  // positions of the workgroup's first and last query, and the keys they see
-  const int ta = (int)(row0 / a.group), tb = (int)((min(row0 + ROWS, rows) - 1) / a.group);
-  const int pa = nk - nq + ta, pb = nk - nq + tb;
-  const int jend = a.right < 0 ? nk : min(nk, max(0, (int)min((int64_t)pb + a.right + 1, (int64_t)nk)));
+  // positions of the first and last query, and the tiles of the keys they see: those of
+  // the sinks that lie before the window's, then the window's
+  const int pa = w.nk - w.nq + divide(w.row0, a.by_group);
+  const int pb = w.nk - w.nq + divide(min(w.row0 + (ROWS - 1), w.rows - 1), a.by_group);
+  const int jend = a.right < 0 ? w.nk : max(0, (int)min((int64_t)pb + a.right + 1, (int64_t)w.nk));
   const int jbeg = a.left < 0 ? 0 : min(max(0, pa - a.left), jend);
-  const int tend = (jend + kKeys - 1) / kKeys;
-  const int tbeg = jbeg / kKeys;
-  const int nsink = min(tbeg, (min(a.sinks, jend) + kKeys - 1) / kKeys);  // tiles of sinks before the window's
-  const int ntiles = nsink + tend - tbeg;
-  const int t_first = (int)((int64_t)ntiles * split / a.splits), t_last = (int)((int64_t)ntiles * (split + 1) / a.splits);
-  auto tile_key = [&](int t) { return (t < nsink ? t : tbeg + t - nsink) * kKeys; };
+  w.tbeg = jbeg / kKeys;
+  w.nsink = min(w.tbeg, (min(a.sinks, jend) + kKeys - 1) / kKeys);
+  const int tiles = w.nsink + (jend + kKeys - 1) / kKeys - w.tbeg;
+  w.t_first = divide(tiles * w.split, a.by_splits);  // (below 2^24 tiles, and 2^6 splits)
+  w.t_last = divide(tiles * (w.split + 1), a.by_splits);
+  return true;
+}
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// A copy of 16 bytes a lane from a buffer to LDS: lane i's, at byte off, lands at lds + 16 i;
+// past the buffer's end it is zeros. In asm, so that the compiler's waits for it (it would
+// wait for all copies before the next LDS read) stay out of the loop, which waits before its
+// barrier. s_nop: M0 needs one wait state before the copy, a resource five if a vector
+// instruction wrote it (the compiler brings a spilled one back with one).
+__device__ __forceinline__ void copy16(const i32x4& rs, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(off), "s"(rs) : "memory", "m0");
+}
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ bf16x8_v lds_row(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8_v*>(at);
+}
+__device__ __forceinline__ s16x4 lds_columns(uint32_t at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4*>(at));
+}
+
+template <int N, class F>
+__device__ __forceinline__ void unroll(F&& f) {
+  [&]<int... I>(std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }(std::make_integer_sequence<int, N>{});
+}
+
+constexpr int LEAD = 4;  // fragments of operand A read ahead
+
+template <int D, int QT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a) {
+  constexpr int ROWS = 32 * QT * NW, CH = D / 8, TILE = kKeys * D * 2, DC = D / 16, DT = D / 32;
+  constexpr int COPIES = TILE / 1024 / NW;  // of 1 KiB, per wave and tensor
+  extern __shared__ __attribute__((aligned(128))) uint8_t lds[];  // [2] of a tile's K, V
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  Work w;
+  if (!find_work<ROWS>(a, lane, w)) return;
+  const int nk = w.nk, ntiles = w.t_last - w.t_first;
+  auto tile_key = [&](int t) {
+    t += w.t_first;
+    return (t < w.nsink ? t : w.tbeg + t - w.nsink) * kKeys;
+  };
+
+  // copies of a tile; rows past the last key are zeros
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const uint16_t* kbase = a.k + (int64_t)w.k0 * a.ldk + w.hk * D;
+  const uint16_t* vbase = a.v + (int64_t)w.k0 * a.ldv + w.hk * D;
+  uint32_t koff[COPIES], voff[COPIES];
+#pragma unroll
+  for (int c = 0; c < COPIES; ++c) {
+    const int piece = (wave * COPIES + c) * 64 + lane, r = piece / CH, at = piece % CH;
+    koff[c] = (uint32_t)(2 * (r * a.ldk + 8 * k_chunk<D>(r, at)));
+    voff[c] = (uint32_t)(2 * (r * a.ldv + 8 * v_chunk<D>(r, at)));
+  }
+  auto tile_rows = [&](const uint16_t* base, int64_t ld, int key) {
+    const uint64_t at = (uint64_t)(base + key * ld);
+    const int last = min(nk - key, kKeys) - 1;  // (64 rows of 2^24 elements stay below 2^31 bytes)
+    i32x4 r;
+    r.x = (int)(uint32_t)at;
+    r.y = (int)(uint32_t)(at >> 32) & 0xFFFF;
+    r.z = last * (int)ld * 2 + 2 * D;
+    r.w = 0x00020000;
+    return r;
+  };
+  // (past the last tile it is copied again, to a place that is not read any more)
+  auto fetch_k = [&](int t, int buf) {
+    const i32x4 rs = tile_rows(kbase, a.ldk, tile_key(min(t, ntiles - 1)));
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) copy16(rs, koff[c], lds0 + buf * 2 * TILE + (wave * COPIES + c) * 1024);
+  };
+  auto fetch_v = [&](int t, int buf) {
+    const i32x4 rs = tile_rows(vbase, a.ldv, tile_key(min(t, ntiles - 1)));
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) copy16(rs, voff[c], lds0 + buf * 2 * TILE + TILE + (wave * COPIES + c) * 1024);
+  };
+
+  // The loop takes two steps a turn (scores and buffers change places without moves) and the
+  // last tile's product follows it: an even number of tiles has its first one out of turn.
+  const int odd = (ntiles - 1) & 1;
+  if (ntiles > 0) {
+    fetch_k(0, odd);
+    fetch_v(0, odd);
+    fetch_k(1, odd ^ 1);
+  }
 
   // this wave's rows
-  int64_t row[QT];
   int pos[QT];
-  const uint16_t* kbase = a.k + (int64_t)k0 * a.ldk + hk * D;
-  const uint16_t* vbase = a.v + (int64_t)k0 * a.ldv + hk * D;
-  bf16x8_v qf[QT][D / 16];
+  bf16x8_v qf[QT][DC];
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
-    row[i] = row0 + (wave * QT + i) * 32 + l32;
-    const int64_t r = min(row[i], rows - 1);
-    const int t = (int)(r / a.group), g = (int)(r - (int64_t)t * a.group);
-    pos[i] = nk - nq + t;
-    const uint16_t* src = a.q + (int64_t)(q0 + t) * a.ldq + (hk * a.group + g) * D + 8 * half;
+    const int r = min(w.row0 + (wave * QT + i) * 32 + l32, w.rows - 1);
+    const int t = divide(r, a.by_group), g = r - t * a.group;
+    pos[i] = nk - w.nq + t;
+    const uint16_t* src = a.q + (int64_t)(w.q0 + t) * a.ldq + (w.hk * a.group + g) * D + 8 * half;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) qf[i][c] = *reinterpret_cast<const bf16x8_v*>(src + 16 * c);
+    for (int c = 0; c < DC; ++c) qf[i][c] = *reinterpret_cast<const bf16x8_v*>(src + 16 * c);
   }
-  const int64_t wrow = row0 + wave * QT * 32;  // positions of the wave's rows
-  const int wpa = nk - nq + (int)(min(wrow, rows - 1) / a.group);
-  const int wpb = nk - nq + (int)(min(wrow + QT * 32 - 1, rows - 1) / a.group);
+  const int wrow = min(w.row0 + wave * QT * 32, w.rows - 1);  // positions of the wave's first and last row
+  const int wpa = nk - w.nq + divide(wrow, a.by_group);
+  const int wpb = nk - w.nq + divide(min(wrow + (QT * 32 - 1), w.rows - 1), a.by_group);
 
-  f32x16 o[QT][D / 32];
-  float m[QT], l[QT];
+  f32x16 o[QT][DT];
+  float m[QT], l[QT], sum[QT][2];
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
     m[i] = -__builtin_inff();
     l[i] = 0.0f;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[i][d][r] = 0.0f;
   }
 
-  // copies of one tile: rows past the last key repeat it
-  auto fetch = [&](int key, int buf) {
-    uint8_t* base = lds + buf * 2 * TILE;
+  // LDS addresses of the lane's operand reads in buffer 0
+  uint32_t ka[DC], va[DT];
 #pragma unroll
-    for (int c = 0; c < COPIES; ++c) {
-      const int piece = wave * COPIES + c;
-      const int r = (piece * 64 + lane) / CH, at = (piece * 64 + lane) % CH;
-      const int64_t key_row = min(key + r, nk - 1);
-      copy16(kbase + key_row * a.ldk + 8 * k_chunk<D>(r, at), base + piece * 1024);
-      copy16(vbase + key_row * a.ldv + 8 * v_chunk<D>(r, at), base + TILE + piece * 1024);
-    }
-  };
+  for (int c = 0; c < DC; ++c) ka[c] = lds0 + l32 * D * 2 + 16 * k_chunk<D>(l32, 2 * c + half);
+#pragma unroll
+  for (int d = 0; d < DT; ++d) {
+    // lanes 16 e .. 16 e + 15 (e = lane / 16) transpose keys 4 (e / 2) .. + 3 at columns 16 (e % 2) ..
+    const int r = 4 * half + ((lane & 15) >> 2), col = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    va[d] = lds0 + TILE + r * D * 2 + 16 * v_chunk<D>(r, col >> 3) + 2 * (col & 7);
+  }
 
-  if (t_first < t_last) fetch(tile_key(t_first), 0);
-  for (int t = t_first; t < t_last; ++t) {
-    const int key = tile_key(t), buf = (t - t_first) & 1;
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (t + 1 < t_last) fetch(tile_key(t + 1), buf ^ 1);
-    // whether the wave's rows see the tile at all, and all of it
-    const bool none = wrow >= rows || (a.right >= 0 && key > (int64_t)wpb + a.right) ||
-                      (a.left >= 0 && key + kKeys - 1 < wpa - a.left && key >= a.sinks);
-    if (none) continue;
-    const bool whole = key + kKeys <= nk && (a.right < 0 || key + kKeys - 1 <= (int64_t)wpa + a.right) &&
-                       (a.left < 0 || key >= wpb - a.left || key + kKeys <= a.sinks);
-    const uint8_t* kt = lds + buf * 2 * TILE;
-    const uint8_t* vt = kt + TILE;
-    f32x16 s[QT][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[i][j][r] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const int r = 32 * j + l32;
-        const bf16x8_v kf = *reinterpret_cast<const bf16x8_v*>(kt + r * D * 2 + 16 * k_chunk<D>(r, 2 * c + half));
-#pragma unroll
-        for (int i = 0; i < QT; ++i) s[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i][c], s[i][j], 0, 0, 0);
-      }
-    }
-    u32x4_v p[QT][2][2];
-#pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      if (!whole) {
-        const int hi = a.right < 0 ? nk - 1 : (int)min((int64_t)nk - 1, (int64_t)pos[i] + a.right);
-        const int lo = a.left < 0 ? 0 : pos[i] - a.left;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int at = key + 32 * j + 8 * (r >> 2) + 4 * half + (r & 3);
-            const bool seen = at <= hi && (at >= lo || at < a.sinks);
-            s[i][j][r] = seen ? s[i][j][r] : -__builtin_inff();
-          }
-      }
-      float top = s[i][0][0];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][j][r]);
-      top = fmaxf(other_half_max(top), m[i]);
-      if (__any(top > m[i])) {
-        const float alpha = top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((m[i] - top) * a.scale_log2);
-        m[i] = top;
-        l[i] *= alpha;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) o[i][d][r] *= alpha;
-      }
-      const float shift = m[i] == -__builtin_inff() ? 0.0f : -m[i] * a.scale_log2;
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][j][r], a.scale_log2, shift));
-          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][j][r + 1], a.scale_log2, shift));
-          sum += e0 + e1;
-          p[i][j][r >> 3][(r & 7) >> 1] = bf16x2_rne(e0, e1);
-        }
-      l[i] += sum;
-    }
+  // scores of a tile
+  auto scores = [&](f32x16 (&s)[QT][2], uint32_t buf) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < DC; ++c) {
+        const bf16x8_v kf = lds_row(ka[c] + buf + j * 32 * D * 2);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
-          // lanes 16 e .. 16 e + 15 (e = lane / 16) transpose keys 4 (e / 2) .. + 3 at columns 16 (e % 2) ..
-          const int r0 = 32 * j + 16 * c + 4 * half + ((lane & 15) >> 2);
-          const int col = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);  // element
-          const uint8_t* at0 = vt + r0 * D * 2 + 16 * v_chunk<D>(r0, col >> 3) + 2 * (col & 7);
-          const uint8_t* at1 = vt + (r0 + 8) * D * 2 + 16 * v_chunk<D>(r0 + 8, col >> 3) + 2 * (col & 7);
-          const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at0);
-          const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at1);
-          const bf16x8_v vf = __builtin_bit_cast(bf16x8_v, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+        for (int i = 0; i < QT; ++i) {
+          f32x16 z;
 #pragma unroll
-          for (int i = 0; i < QT; ++i)
-            o[i][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8_v, p[i][j][c]), o[i][d], 0, 0, 0);
+          for (int r = 0; r < 16; ++r) z[r] = 0.0f;
+          s[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i][c], c == 0 ? z : s[i][j], 0, 0, 0);
         }
+      }
+  };
+  auto maxima = [&](const f32x16 (&s)[QT][2], float (&top)[QT]) {
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      float x = s[i][0][0];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x = fmaxf(x, s[i][j][r]);
+      top[i] = other_half_max(x);
+    }
+  };
+  // hides what the wave's rows do not see of a tile; false if that is nothing
+  auto hide = [&](f32x16 (&s)[QT][2], int key) {
+    const bool whole = key + kKeys <= nk && (a.right < 0 || key + kKeys - 1 <= (int64_t)wpa + a.right) &&
+                       (a.left < 0 || key >= wpb - a.left || key + kKeys <= a.sinks);
+    if (whole) return false;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      const int hi = a.right < 0 ? nk - 1 : (int)min((int64_t)nk - 1, (int64_t)pos[i] + a.right);
+      const int lo = a.left < 0 ? 0 : pos[i] - a.left;
+      int first = key + 4 * half;
+      asm volatile("" : "+v"(first));  // (else the 32 sums below are kept in registers over the loop)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int at = first + 32 * j + 8 * (r >> 2) + (r & 3);
+          const bool seen = at <= hi && (at >= lo || at < a.sinks);
+          s[i][j][r] = seen ? s[i][j][r] : -__builtin_inff();
+        }
+    }
+    return true;
+  };
+  // raises the running maximum where the tile's is far above it
+  auto raise = [&](const float (&top)[QT]) {
+    bool up = false;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) up |= top[i] > m[i] + a.slack;
+    if (!__any(up)) return;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      const float now = fmaxf(top[i], m[i]);
+      const float alpha = now == m[i] ? 1.0f : __builtin_amdgcn_exp2f((m[i] - now) * a.scale_log2);
+      m[i] = now;
+      sum[i][0] *= alpha;
+      sum[i][1] *= alpha;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][d][r] *= alpha;
+    }
+  };
+  // operand A of a step: its key fragments (of the next tile), then its value fragments
+  constexpr int F1 = 2 * DC, F2 = 4 * DT, F = F1 + F2, SLOTS = F * QT;
+  auto key_fragment = [&](int f, uint32_t buf) { return lds_row(ka[f % DC] + buf + (f / DC) * 32 * D * 2); };
+  auto value_fragment = [&](int f, uint32_t buf) {
+    const uint32_t at = va[f % DT] + buf + (f / DT) * 16 * D * 2;
+    const s16x4 v0 = lds_columns(at), v1 = lds_columns(at + 8 * D * 2);
+    return __builtin_bit_cast(bf16x8_v, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  // vector work of a step, instruction by instruction: per pair of scores the exponents'
+  // arguments, the weights, and (of the pair before) their sums and bf16 values; then the
+  // maxima of the next tile's scores
+  constexpr int PER_PAIR = 7, PAIRS = 16 * QT, OPS_W = PER_PAIR * (PAIRS + 1), OPS_M = 16 * QT;
+  // the weights of the last 16 keys are needed in slot W: all weights come before it,
+  // evenly, and the maxima after them
+  constexpr int W = (F1 + 3 * DT) * QT;
+  static_assert(PER_PAIR * (12 * QT + 1) * W < (F1 + 2 * DT) * QT * OPS_W && PER_PAIR * (8 * QT + 1) * W < (F1 + DT) * QT * OPS_W &&
+                PER_PAIR * (4 * QT + 1) * W < F1 * QT * OPS_W);
+  auto ops_before = [](int slot) constexpr {
+    return slot <= W ? slot * OPS_W / W : OPS_W + (slot - W) * OPS_M / (SLOTS - W);
+  };
+  float shift[QT];
+  float e[2][2], arg[2];
+  u32x4_v p[QT][4];
+  float top[QT];
+  auto vector_op = [&](auto op, f32x16 (&cur)[QT][2], f32x16 (&nxt)[QT][2]) {
+    constexpr int n = op;
+    if constexpr (n < OPS_W) {
+      constexpr int k = n / PER_PAIR, what = n % PER_PAIR;
+      if constexpr (what < 4 && k < PAIRS) {
+        constexpr int jc = k / (4 * QT), i = k / 4 % QT, r = 8 * (jc & 1) + 2 * (k & 3) + (what & 1);
+        if constexpr (what < 2)
+          arg[what] = __builtin_fmaf(cur[i][jc >> 1][r], a.scale_log2, shift[i]);
+        else
+          e[k & 1][what & 1] = __builtin_amdgcn_exp2f(arg[what & 1]);
+      } else if constexpr (what >= 4 && k > 0) {
+        constexpr int b = k - 1, i = b / 4 % QT;
+        if constexpr (what < 6) {
+          sum[i][what - 4] += e[b & 1][what - 4];
+          asm volatile("" : "+v"(sum[i][what - 4]));  // (stays here: the compiler would move the sums behind the step)
+        } else {
+          p[i][b / (4 * QT)][b & 3] = bf16x2_rne(e[b & 1][0], e[b & 1][1]);
+        }
+      }
+    } else {
+      constexpr int k = n - OPS_W, i = k / 16, r = 2 * (k % 16);
+      const float x = nxt[i][r >> 4][r & 15], y = nxt[i][(r + 1) >> 4][(r + 1) & 15];
+      top[i] = r == 0 ? fmaxf(x, y) : fmaxf(fmaxf(top[i], x), y);
+      asm volatile("" : "+v"(top[i]));
+    }
+  };
+  static_assert(F % LEAD == 0);  // (fragment n is always ring[n % LEAD])
+  bf16x8_v ring[LEAD];
+
+  if (ntiles > 0) {
+    f32x16 sa[QT][2], sb[QT][2];
+    auto shifts = [&] {
+#pragma unroll
+      for (int i = 0; i < QT; ++i) shift[i] = m[i] == -__builtin_inff() ? 0.0f : -m[i] * a.scale_log2;
+    };
+    auto first_scores = [&](int t, uint32_t buf) {
+      scores(sa, buf);
+      hide(sa, tile_key(t));
+      maxima(sa, top);
+      raise(top);
+    };
+    // a tile's weights and product by themselves
+    auto product = [&](uint32_t buf) {
+      shifts();
+      unroll<OPS_W>([&](auto n) { vector_op(n, sa, sb); });
+      unroll<F2>([&](auto f) {
+        const bf16x8_v vf = value_fragment(f, buf);
+#pragma unroll
+        for (int i = 0; i < QT; ++i)
+          o[i][f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8_v, p[i][f / DT]), o[i][f % DT], 0, 0, 0);
+      });
+    };
+#pragma unroll
+    for (int i = 0; i < QT; ++i) sum[i][0] = sum[i][1] = 0.0f;
+    tile_barrier();
+    first_scores(0, odd * 2 * TILE);
+    tile_barrier();  // (the first keys are read: their place takes the third tile's)
+    fetch_k(2, odd);
+    fetch_v(1, odd ^ 1);
+    if (odd) {
+      product(2 * TILE);
+      first_scores(1, 0);
+      tile_barrier();
+      fetch_k(3, 0);
+      fetch_v(2, 1);
+    }
+    unroll<LEAD>([&](auto f) { ring[f] = key_fragment(f, 2 * TILE); });
+
+    // Step t: scores of tile t + 1 (nxt) and, from those of tile t (cur), its weights and
+    // their product with the values. Each MFMA is followed by its share of the vector work
+    // and by the read of the fragment LEAD ahead; LEAD fragments before the end all reads of
+    // the step are done and the workgroup meets: the step's tiles give way to those two
+    // further, and the next step's fragments are read.
+    auto step = [&](f32x16 (&cur)[QT][2], f32x16 (&nxt)[QT][2], int t, auto par) {
+      constexpr uint32_t kbuf = (par ^ 1) * 2 * TILE, vbuf = par * 2 * TILE, next_k = par * 2 * TILE;
+      shifts();
+      unroll<SLOTS>([&](auto slot) {
+        constexpr int f = slot / QT, i = slot % QT;
+        if constexpr (f == F - LEAD && i == 0) {
+          tile_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (f < F1) {
+          f32x16 z;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) z[r] = 0.0f;
+          nxt[i][f / DC] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], qf[i][f % DC],
+                                                                   f % DC == 0 ? z : nxt[i][f / DC], 0, 0, 0);
+        } else {
+          constexpr int g = f - F1;
+          o[i][g % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], __builtin_bit_cast(bf16x8_v, p[i][g / DT]),
+                                                                 o[i][g % DT], 0, 0, 0);
+        }
+        if constexpr (i == QT - 1) {
+          constexpr int n = f + LEAD;
+          if constexpr (n < F1)
+            ring[f % LEAD] = key_fragment(n, kbuf);
+          else if constexpr (n < F)
+            ring[f % LEAD] = value_fragment(n - F1, vbuf);
+          else
+            ring[f % LEAD] = key_fragment(n - F, next_k);
+        }
+        constexpr int first = ops_before(slot), last = ops_before(slot + 1);
+        if constexpr (f == F - LEAD && i == QT - 1) fetch_k(t + 3, par ^ 1);
+        if constexpr (f == F - LEAD + 1 && i == QT - 1) fetch_v(t + 2, par);
+        unroll<last - first>([&](auto n) { vector_op(std::integral_constant<int, first + n>{}, cur, nxt); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+#pragma unroll
+      for (int i = 0; i < QT; ++i) top[i] = other_half_max(top[i]);
+      if (hide(nxt, tile_key(t + 1))) maxima(nxt, top);
+      raise(top);
+    };
+    for (int t = odd; t < ntiles - 1; t += 2) {
+      step(sa, sb, t, std::integral_constant<int, 0>{});
+      step(sb, sa, t + 1, std::integral_constant<int, 1>{});
+    }
+    tile_barrier();
+    product(0);
+#pragma unroll
+    for (int i = 0; i < QT; ++i) l[i] = sum[i][0] + sum[i][1];
   }
 
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
     l[i] = other_half_sum(l[i]);
-    if (row[i] >= rows) continue;
-    const int t = (int)(row[i] / a.group), g = (int)(row[i] - (int64_t)t * a.group);
+    const int row = w.row0 + (wave * QT + i) * 32 + l32;
+    const int t = divide(min(row, w.rows - 1), a.by_group), g = row - t * a.group;
     if (a.splits > 1) {
+      if (row >= w.rows) continue;
       // unnormalised part: D sums, the maximum (in units of log2) and the sum of weights
-      const int64_t at = ((int64_t)split * a.Mq + q0 + t) * (a.kv_heads * a.group) + hk * a.group + g;
+      const int64_t at = ((int64_t)w.split * a.Mq + w.q0 + t) * (a.kv_heads * a.group) + w.hk * a.group + g;
       float* dst = a.part + at * D;
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 16; r += 4)
           *reinterpret_cast<float4*>(dst + 32 * d + 2 * r + 4 * half) = make_float4(o[i][d][r], o[i][d][r + 1], o[i][d][r + 2], o[i][d][r + 3]);
@@ -279,61 +501,97 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs a) {
       }
     } else {
       const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-      uint16_t* dst = a.out + (int64_t)(q0 + t) * a.ldo + (hk * a.group + g) * D;
+      uint16_t* dst = a.out + (int64_t)(w.q0 + t) * a.ldo + (w.hk * a.group + g) * D + 8 * half;
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          *reinterpret_cast<uint2*>(dst + 32 * d + 2 * r + 4 * half) =
-              make_uint2(bf16x2_rne(o[i][d][r] * inv, o[i][d][r + 1] * inv), bf16x2_rne(o[i][d][r + 2] * inv, o[i][d][r + 3] * inv));
+        for (int r = 0; r < 16; r += 8) {
+          // elements 8 half .. + 7 of 16: the halves' second and first four change places
+          uint32_t x[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) x[h] = bf16x2_rne(o[i][d][r + 2 * h] * inv, o[i][d][r + 2 * h + 1] * inv);
+          const u32x2_v y0 = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
+          const u32x2_v y1 = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
+          if (row < w.rows) *reinterpret_cast<uint4*>(dst + 32 * d + 2 * r) = make_uint4(y0[0], y1[0], y0[1], y1[1]);
+        }
     }
   }
 }
 
-// Joins the parts of a row: weights 2^(m_s - max). A wave per 64 / (D / 4) rows.
+// Joins the parts of a row, weights 2^(m_s - max): D / 4 threads to a row and a quarter of
+// its parts, the quarters joined in LDS.
+constexpr int kJoin = 4;
+
 template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs a) {
-  constexpr int LANES = D / 4;
+  constexpr int LANES = D / 4, ROWS = 256 / LANES / kJoin;
+  __shared__ __attribute__((aligned(16))) float so[ROWS][kJoin][D];
+  __shared__ float sml[ROWS][kJoin][2];
   const int heads = a.kv_heads * a.group;
   const int end = a.starts_q != nullptr ? min(max(a.starts_q[a.sequences], 0), a.Mq) : a.Mq;
   const int begin = a.starts_q != nullptr ? min(max(a.starts_q[0], 0), a.Mq) : 0;
-  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
-  const int c = (threadIdx.x % LANES) * 4;
+  const int local = threadIdx.x / (LANES * kJoin), which = threadIdx.x / LANES % kJoin, c = (threadIdx.x % LANES) * 4;
+  const int64_t r = (int64_t)blockIdx.x * ROWS + local;
   const int64_t row = r / heads;
-  if (row < begin || row >= end) return;
+  const bool live = row >= begin && row < end;
   const int64_t total = (int64_t)a.Mq * heads;
   const float* ml = a.part + a.splits * total * D;
-  float top = -__builtin_inff();
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, ml[2 * (s * total + r)]);
-  const float at = top == -__builtin_inff() ? 0.0f : top;
-  float l = 0.0f;
+  float top = -__builtin_inff(), l = 0.0f;
   float4 o = make_float4(0, 0, 0, 0);
-  for (int s = 0; s < a.splits; ++s) {
-    const float w = __builtin_amdgcn_exp2f(ml[2 * (s * total + r)] - at);
-    const float4 v = *reinterpret_cast<const float4*>(a.part + (s * total + r) * D + c);
-    l += w * ml[2 * (s * total + r) + 1];
-    o.x += w * v.x;
-    o.y += w * v.y;
-    o.z += w * v.z;
-    o.w += w * v.w;
+  auto add = [&](float pm, float pl, const float4& v) {
+    const float now = fmaxf(top, pm);
+    const float at = now == -__builtin_inff() ? 0.0f : now;
+    const float f = __builtin_amdgcn_exp2f(top - at), w = __builtin_amdgcn_exp2f(pm - at);
+    top = now;
+    l = l * f + pl * w;
+    o.x = o.x * f + v.x * w;
+    o.y = o.y * f + v.y * w;
+    o.z = o.z * f + v.z * w;
+    o.w = o.w * f + v.w * w;
+  };
+  if (live)
+#pragma unroll 4
+    for (int s = which; s < a.splits; s += kJoin) {
+      const float2 p = *reinterpret_cast<const float2*>(ml + 2 * (s * total + r));
+      add(p.x, p.y, *reinterpret_cast<const float4*>(a.part + (s * total + r) * D + c));
+    }
+  *reinterpret_cast<float4*>(&so[local][which][c]) = o;
+  if (c == 0) {
+    sml[local][which][0] = top;
+    sml[local][which][1] = l;
   }
+  __syncthreads();
+  if (which != 0 || !live) return;
+#pragma unroll
+  for (int s = 1; s < kJoin; ++s) add(sml[local][s][0], sml[local][s][1], *reinterpret_cast<const float4*>(&so[local][s][c]));
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   *reinterpret_cast<uint2*>(a.out + row * a.ldo + (r - row * heads) * D + c) =
       make_uint2(bf16x2_rne(o.x * inv, o.y * inv), bf16x2_rne(o.z * inv, o.w * inv));
 }
 
-constexpr int kQT = 1, kNW = 8, kRows = 32 * kQT * kNW;
-
-static int64_t attention_slots(const mxq_attention_args& g) {
-  return g.Mq * (g.heads / g.kv_heads) / kRows + g.sequences;
+// Workgroups of four waves and 128 rows, two on a CU, which fill each other's waits; of
+// eight waves and 256 rows (a key tile is copied half as often) where heads are 128 long
+// and a row sees some 6000 keys. 40 heads of 128, four waves against eight: 2048 x 2048
+// 93 and 108 us, 4096 x 4096 304 and 318, 8192 x 8192 1173 and 1127, 32760 x 32760 18.6
+// and 18.0 ms. 64 heads of 64, 16384 x 16384: 4.39 and 4.59 ms (the exponentials bound it).
+static int attention_waves(const mxq_attention_args& g) {
+  const int64_t per = g.sequences > 0 ? g.Mk / g.sequences : 0;
+  const int64_t seen = g.left >= 0 && g.right >= 0 && g.left + g.right < per ? g.left + g.right : per;
+  return g.head_dim == 128 && seen >= 6144 ? 8 : 4;
 }
 
+static int64_t attention_slots(const mxq_attention_args& g) {
+  return g.Mq * (g.heads / g.kv_heads) / (32 * attention_waves(g)) + g.sequences;
+}
+
+// Parts of the keys, so that few rows fill the chip, each of at least 8 tiles.
 static int attention_splits(const mxq_attention_args& g) {
   const int64_t items = attention_slots(g) * g.kv_heads;
-  const int64_t tiles = (g.Mk + kKeys - 1) / kKeys;
   if (items == 0) return 1;
-  int64_t s = 512 / items;
+  int64_t s = 256 * (8 / attention_waves(g)) / items;
+  const int64_t tiles = (g.Mk + kKeys - 1) / kKeys;
   if (s > tiles / 8) s = tiles / 8;
+  if (s > 64) s = 64;
   return s < 2 ? 1 : (int)s;
 }
 
@@ -343,16 +601,16 @@ size_t attention_workspace(const mxq_attention_args& g) {
 }
 
 bool attention_fits(const mxq_attention_args& g) {
-  return (attention_slots(g) * g.kv_heads * attention_splits(g) + 8) * 64 * kNW < (int64_t(1) << 32);
+  return g.Mq * (g.heads / g.kv_heads) < (int64_t(1) << 31) - 256 &&
+         (attention_slots(g) * g.kv_heads * attention_splits(g) + 8) * 64 * attention_waves(g) < (int64_t(1) << 32);
 }
 
-template <int D>
+template <int D, int NW>
 static hipError_t launch(const AttnArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)((a.items + 7) / 8 * 8);
-  hipLaunchKernelGGL((attention_kernel<D, kQT, kNW>), dim3(grid), dim3(64 * kNW), 4 * kKeys * D * 2, s, a);
+  hipLaunchKernelGGL((attention_kernel<D, 1, NW>), dim3((unsigned)((a.items + 7) / 8 * 8)), dim3(64 * NW), 4 * kKeys * D * 2, s, a);
   if (a.splits > 1) {
-    const int64_t rows = (int64_t)a.Mq * a.kv_heads * a.group;
-    hipLaunchKernelGGL((attention_join_kernel<D>), dim3((unsigned)((rows * (D / 4) + 255) / 256)), dim3(256), 0, s, a);
+    const int64_t rows = (int64_t)a.Mq * a.kv_heads * a.group, per = 256 / (D / 4) / kJoin;
+    hipLaunchKernelGGL((attention_join_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
@@ -374,8 +632,13 @@ hipError_t launch_attention(const mxq_attention_args& g, void* workspace, hipStr
   a.slots = (int)attention_slots(g);
   a.splits = attention_splits(g);
   a.items = a.slots * a.kv_heads * a.splits;
+  a.by_group = divider(a.group);
+  a.by_slots = divider(a.slots);
+  a.by_splits = divider(a.splits);
   a.scale_log2 = g.scale * 1.4426950408889634f;
-  return g.head_dim == 128 ? launch<128>(a, s) : launch<64>(a, s);
+  a.slack = 8.0f / a.scale_log2;
+  if (g.head_dim == 64) return launch<64, 4>(a, s);
+  return attention_waves(g) == 8 ? launch<128, 8>(a, s) : launch<128, 4>(a, s);
 }
 
 }  // namespace mxq

@@ -43,7 +43,7 @@ struct RotaryArgs {
   uint8_t* cvs;
   int64_t M, ldx, ldq, ldk, ld_pos, capacity, rows_per_wg;
   int heads, kv_heads, dshift, axes, pairs, interleaved, norm, page_shift, mxfp8, units;
-  float eps;
+  float eps, inv_q, inv_k;  // (inverse elements of a row's q and k)
 };
 
 // Sum and maximum over the 8 (head size 128) or 4 (64) lanes of a head.
@@ -84,10 +84,38 @@ __device__ __forceinline__ uint32_t mxfp8_scale_byte(uint32_t amax_bits) {
   return b < 0 ? 0u : (uint32_t)b;
 }
 
+// Rotations of 8 elements by the pairs' cosines and sines: four pairs side by side,
+// or eight pairs of one chunk with the other.
+__device__ __forceinline__ void turn_interleaved(float (&f)[8], const float* cs, const float* sn) {
+  const float4 c = *reinterpret_cast<const float4*>(cs), s = *reinterpret_cast<const float4*>(sn);
+  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float x = f[2 * p], y = f[2 * p + 1];
+    f[2 * p] = x * cc[p] - y * ss[p];
+    f[2 * p + 1] = x * ss[p] + y * cc[p];
+  }
+}
+__device__ __forceinline__ void turn_halves(float (&f)[8], float (&g)[8], const float* cs, const float* sn) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + 4 * h), s = *reinterpret_cast<const float4*>(sn + 4 * h);
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float x = f[4 * h + p], y = g[4 * h + p];
+      f[4 * h + p] = x * cc[p] - y * ss[p];
+      g[4 * h + p] = x * ss[p] + y * cc[p];
+    }
+  }
+}
+
 template <int U, int R>
 __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
-  __shared__ __attribute__((aligned(16))) float turn[R][2][kMaxPairs];  // cosines, sines
-  __shared__ float red[R][2][16];                                       // waves' sums of q and of k
+  // cosines and sines of R tokens, and the waves' sums of q and of k: double-buffered, so
+  // that the one barrier of a step also frees the buffer of the step before
+  __shared__ __attribute__((aligned(16))) float turn[2][R][2][kMaxPairs];
+  __shared__ float red[2][R][2][16];
   const int tid = threadIdx.x, T = blockDim.x, lane = tid & 63, wave = tid >> 6, waves = T >> 6;
   const int D = 1 << a.dshift, per_head = D >> 4;
   const bool wide = per_head == 8;
@@ -95,22 +123,34 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
   const int64_t begin = (int64_t)blockIdx.x * a.rows_per_wg;
   const int64_t end = begin + a.rows_per_wg < a.M ? begin + a.rows_per_wg : a.M;
 
-  // the thread's units: part (0 q, 1 k, 2 v, 3 none), head, first elements of the two chunks
-  int part[U], head[U], c0[U], c1[U], first_pair[U];
+  // the thread's units: part (0 q, 1 k, 2 v, 3 none), head, first elements of the two
+  // chunks, first pairs of the chunks (interleaved) or of the unit; -1: not turned
+  int part[U], head[U], c0[U], c1[U], p0[U], p1[U];
+  int64_t from[U];
   uint4 w0[U], w1[U];
   const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    int at = tid + T * u;
+    int at = (int)blockIdx.y * T + tid + T * u;
     part[u] = at >= a.units ? 3 : at < qn ? 0 : at < qn + kn ? 1 : 2;
     at -= part[u] == 1 ? qn : part[u] == 2 ? qn + kn : 0;
     const int sub = at & (per_head - 1);
     head[u] = part[u] == 3 ? 0 : at / per_head;
-    const bool turned = 8 * sub < a.pairs && part[u] < 2;
-    first_pair[u] = turned ? 8 * sub : -1;
-    const bool apart = !a.interleaved && 8 * sub < a.pairs;
-    c0[u] = apart ? 8 * sub : 16 * sub;
-    c1[u] = apart ? a.pairs + 8 * sub : 16 * sub + 8;
+    c0[u] = 8 * sub;
+    c1[u] = D / 2 + 8 * sub;
+    p0[u] = p1[u] = -1;
+    if (a.interleaved) {
+      if (c0[u] < 2 * a.pairs) p0[u] = c0[u] / 2;
+      if (c1[u] < 2 * a.pairs) p1[u] = c1[u] / 2;
+    } else if (8 * sub < a.pairs) {
+      c1[u] = a.pairs + 8 * sub;
+      p0[u] = 8 * sub;
+    } else {
+      c0[u] = 16 * sub;
+      c1[u] = 16 * sub + 8;
+    }
+    if (part[u] >= 2) p0[u] = p1[u] = -1;
+    from[u] = (int64_t)(head[u] + (part[u] == 1 ? a.heads : part[u] == 2 ? a.heads + a.kv_heads : 0)) << a.dshift;
     w0[u] = w1[u] = ones;
     const uint16_t* w = part[u] == 0 ? a.q_weight : part[u] == 1 ? a.k_weight : nullptr;
     if (w != nullptr) {
@@ -119,35 +159,53 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
       w1[u] = *reinterpret_cast<const uint4*>(w + c1[u]);
     }
   }
-
-  for (int64_t m0 = begin; m0 < end; m0 += R) {
-    uint4 x0[U][R], x1[U][R];
+  // the pair (and row of a step) whose angle this thread computes
+  const int mine = tid % kMaxPairs, mine_row = tid / kMaxPairs;
+  const bool turns = mine_row < R && mine < a.pairs;
+  double freq = 0.0;
+  const int32_t* pos = nullptr;
+  if (turns) {
+    const int axis = a.axis == nullptr ? 0 : a.axis[mine];
+    if ((unsigned)axis < (unsigned)a.axes) {
+      freq = a.freqs[mine];
+      pos = a.positions + axis * a.ld_pos;
+    }
+  }
+  auto position = [&](int64_t m0) {
+    const int64_t m = m0 + mine_row < end ? m0 + mine_row : end - 1;
+    return pos != nullptr ? pos[m] : 0;
+  };
+  auto load = [&](int64_t m0, uint4 (&x0)[U][R], uint4 (&x1)[U][R]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint16_t* row = a.qkv + (m0 + r < end ? m0 + r : end - 1) * a.ldx;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t at = (int64_t)(head[u] + (part[u] == 1 ? a.heads : part[u] == 2 ? a.heads + a.kv_heads : 0)) << a.dshift;
+        x0[u][r] = x1[u][r] = make_uint4(0, 0, 0, 0);
         if (part[u] < 3) {
-          x0[u][r] = *reinterpret_cast<const uint4*>(row + at + c0[u]);
-          x1[u][r] = *reinterpret_cast<const uint4*>(row + at + c1[u]);
-        } else {
-          x0[u][r] = x1[u][r] = make_uint4(0, 0, 0, 0);
+          x0[u][r] = *reinterpret_cast<const uint4*>(row + from[u] + c0[u]);
+          x1[u][r] = *reinterpret_cast<const uint4*>(row + from[u] + c1[u]);
         }
       }
     }
-    __syncthreads();  // the last rows' angles and sums are read
-    for (int i = tid; i < R * a.pairs; i += T) {
-      const int r = i / a.pairs, p = i - r * a.pairs;
-      const int64_t m = m0 + r < end ? m0 + r : end - 1;
-      const int axis = a.axis == nullptr ? 0 : a.axis[p];
-      double rev = 0.0;
-      if ((unsigned)axis < (unsigned)a.axes)
-        rev = (double)a.positions[axis * a.ld_pos + m] * a.freqs[p] * 0.15915494309189533577;
+  };
+
+  uint4 x0[U][R], x1[U][R], n0[U][R], n1[U][R];
+  load(begin, x0, x1);
+  int at_pos = position(begin), next_pos = 0;
+  int buf = 0;
+  for (int64_t m0 = begin; m0 < end; m0 += R, buf ^= 1) {
+    // the next rows' loads are under way during the arithmetic on these (the last step's
+    // are its own again; in place that is safe: nothing of them is used)
+    const int64_t next = m0 + R < end ? m0 + R : m0;
+    load(next, n0, n1);
+    next_pos = position(next);
+    if (turns) {
+      const double rev = (double)at_pos * freq * 0.15915494309189533577;
       float s, c;
       sincospif(2.0f * (float)(rev - __builtin_rint(rev)), &s, &c);
-      turn[r][0][p] = c;
-      turn[r][1][p] = s;
+      turn[buf][mine_row][0][mine] = c;
+      turn[buf][mine_row][1][mine] = s;
     }
     if (a.norm == MXQ_ROTARY_NORM_ROW) {
 #pragma unroll
@@ -169,8 +227,8 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
           sk += __shfl_xor(sk, off);
         }
         if (lane == 0) {
-          red[r][0][wave] = sq;
-          red[r][1][wave] = sk;
+          red[buf][r][0][wave] = sq;
+          red[buf][r][1][wave] = sk;
         }
       }
     }
@@ -183,11 +241,11 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
       if (a.norm == MXQ_ROTARY_NORM_ROW) {
         float sq = 0.0f, sk = 0.0f;
         for (int w = 0; w < waves; ++w) {
-          sq += red[r][0][w];
-          sk += red[r][1][w];
+          sq += red[buf][r][0][w];
+          sk += red[buf][r][1][w];
         }
-        iq = 1.0f / __builtin_sqrtf(sq / (float)(a.heads << a.dshift) + a.eps);
-        ik = 1.0f / __builtin_sqrtf(sk / (float)(a.kv_heads << a.dshift) + a.eps);
+        iq = __builtin_amdgcn_rsqf(sq * a.inv_q + a.eps);
+        ik = __builtin_amdgcn_rsqf(sk * a.inv_k + a.eps);
       }
       int64_t slot = -1;
       if (a.ck != nullptr) {
@@ -204,7 +262,7 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
           float s = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) s += f[e] * f[e] + g[e] * g[e];
-          inv = 1.0f / __builtin_sqrtf(head_sum(s, wide) * (wide ? 1.0f / 128.0f : 1.0f / 64.0f) + a.eps);
+          inv = __builtin_amdgcn_rsqf(head_sum(s, wide) * (wide ? 1.0f / 128.0f : 1.0f / 64.0f) + a.eps);
         }
         uint4 y0 = x0[u][r], y1 = x1[u][r];
         if (part[u] < 2) {
@@ -218,32 +276,13 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
               g[e] = g[e] * inv * w[e];
             }
           }
-          if (first_pair[u] >= 0) {
-            float c[8], s[8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 cc = *reinterpret_cast<const float4*>(&turn[r][0][first_pair[u] + 4 * h]);
-              const float4 ss = *reinterpret_cast<const float4*>(&turn[r][1][first_pair[u] + 4 * h]);
-              c[4 * h] = cc.x; c[4 * h + 1] = cc.y; c[4 * h + 2] = cc.z; c[4 * h + 3] = cc.w;
-              s[4 * h] = ss.x; s[4 * h + 1] = ss.y; s[4 * h + 2] = ss.z; s[4 * h + 3] = ss.w;
-            }
-            if (a.interleaved) {
-#pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                const float fa = f[2 * p], fb = f[2 * p + 1], ga = g[2 * p], gb = g[2 * p + 1];
-                f[2 * p] = fa * c[p] - fb * s[p];
-                f[2 * p + 1] = fa * s[p] + fb * c[p];
-                g[2 * p] = ga * c[4 + p] - gb * s[4 + p];
-                g[2 * p + 1] = ga * s[4 + p] + gb * c[4 + p];
-              }
-            } else {
-#pragma unroll
-              for (int p = 0; p < 8; ++p) {
-                const float fa = f[p], gb = g[p];
-                f[p] = fa * c[p] - gb * s[p];
-                g[p] = fa * s[p] + gb * c[p];
-              }
-            }
+          const float* cs = turn[buf][r][0];
+          const float* sn = turn[buf][r][1];
+          if (a.interleaved) {
+            if (p0[u] >= 0) turn_interleaved(f, cs + p0[u], sn + p0[u]);
+            if (p1[u] >= 0) turn_interleaved(g, cs + p1[u], sn + p1[u]);
+          } else if (p0[u] >= 0) {
+            turn_halves(f, g, cs + p0[u], sn + p0[u]);
           }
           y0 = make_uint4(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7]));
           y1 = make_uint4(bf16x2_rne(g[0], g[1]), bf16x2_rne(g[2], g[3]), bf16x2_rne(g[4], g[5]), bf16x2_rne(g[6], g[7]));
@@ -255,7 +294,7 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
           }
         }
         if (slot < 0) continue;  // (all lanes of the workgroup alike)
-        uint32_t sb0 = 0, sb1 = 0, mine = 0;
+        uint32_t sb0 = 0, sb1 = 0, kept = 0;
         if (a.mxfp8) {
           // largest magnitudes of the head's blocks of 32; lane j of a head keeps block j's
           const uint32_t m0b = chunk_amax(y0), m1b = chunk_amax(y1);
@@ -264,18 +303,18 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
             const uint32_t byte = mxfp8_scale_byte(here);
             sb0 = c0[u] >> 5 == b ? byte : sb0;
             sb1 = c1[u] >> 5 == b ? byte : sb1;
-            mine = (lane & (per_head - 1)) == b ? byte : mine;
+            kept = (lane & (per_head - 1)) == b ? byte : kept;
           }
         }
         if (part[u] == 1 || part[u] == 2) {
-          const int64_t line =
-              ((slot >> a.page_shift) * a.kv_heads + head[u]) * (int64_t(1) << a.page_shift) + (slot & ((int64_t(1) << a.page_shift) - 1));
+          const int64_t page = int64_t(1) << a.page_shift;
+          const int64_t line = ((slot >> a.page_shift) * a.kv_heads + head[u]) * page + (slot & (page - 1));
           uint8_t* codes = part[u] == 1 ? a.ck : a.cv;
           if (a.mxfp8) {
             *reinterpret_cast<uint2*>(codes + line * D + c0[u]) = pack8_mxfp8(y0, sb0);
             *reinterpret_cast<uint2*>(codes + line * D + c1[u]) = pack8_mxfp8(y1, sb1);
             const int j = lane & (per_head - 1);
-            if (j < D / 32) (part[u] == 1 ? a.cks : a.cvs)[line * (D / 32) + j] = (uint8_t)mine;
+            if (j < D / 32) (part[u] == 1 ? a.cks : a.cvs)[line * (D / 32) + j] = (uint8_t)kept;
           } else {
             uint16_t* out = reinterpret_cast<uint16_t*>(codes) + line * D;
             *reinterpret_cast<uint4*>(out + c0[u]) = y0;
@@ -284,12 +323,20 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
         }
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        x0[u][r] = n0[u][r];
+        x1[u][r] = n1[u][r];
+      }
+    at_pos = next_pos;
   }
 }
 
 template <int U, int R>
-static hipError_t launch(const RotaryArgs& a, unsigned grid, int threads, hipStream_t s) {
-  hipLaunchKernelGGL((rotary_qkv_kernel<U, R>), dim3(grid), dim3(threads), 0, s, a);
+static hipError_t launch(const RotaryArgs& a, dim3 grid, int threads, hipStream_t s) {
+  hipLaunchKernelGGL((rotary_qkv_kernel<U, R>), grid, dim3(threads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -306,6 +353,8 @@ hipError_t launch_rotary_qkv(const mxq_rotary_args& g, const mxq_kv_cache* cache
   a.M = g.M; a.ldx = g.ldx; a.ldq = g.ldq; a.ldk = g.ldk; a.ld_pos = g.ld_pos;
   a.heads = g.heads; a.kv_heads = g.kv_heads; a.dshift = __builtin_ctz((unsigned)g.head_dim);
   a.axes = g.axes; a.pairs = g.pairs; a.interleaved = g.interleaved; a.norm = g.norm; a.eps = g.eps;
+  a.inv_q = 1.0f / (float)(g.heads > 0 ? g.heads * g.head_dim : 1);
+  a.inv_k = 1.0f / (float)(g.kv_heads > 0 ? g.kv_heads * g.head_dim : 1);
   const int per_head = g.head_dim / 16;
   a.units = (g.heads + g.kv_heads) * per_head;
   if (cache != nullptr) {
@@ -319,14 +368,20 @@ hipError_t launch_rotary_qkv(const mxq_rotary_args& g, const mxq_kv_cache* cache
     a.mxfp8 = cache->format == MXQ_KV_MXFP8;
     a.units += g.kv_heads * per_head;
   }
-  const int U = a.units <= 512 ? 1 : a.units <= 1024 ? 2 : 4;
-  const int threads = ((a.units + U - 1) / U + 63) / 64 * 64;
+  // A row's sums need the whole row in one workgroup; heads on their own (or no norm) go to
+  // workgroups of 512 units.
+  const bool row_norm = g.norm == MXQ_ROTARY_NORM_ROW;
+  const int parts = row_norm ? 1 : (a.units + 511) / 512;
+  const int units = (a.units + parts - 1) / parts;
+  const int U = units <= 1024 ? 1 : units <= 2048 ? 2 : 4;
   const int R = g.M < 2048 || U > 1 ? 1 : 2;
+  int threads = ((units + U - 1) / U + 63) / 64 * 64;
+  if (threads < R * kMaxPairs) threads = R * kMaxPairs;
   const int64_t steps = (g.M + R - 1) / R;
-  const int64_t most = 256 * (2048 / threads);
+  const int64_t most = 256 * (1024 / threads);
   const int64_t grid = steps < most ? steps : most;
   a.rows_per_wg = (steps + grid - 1) / grid * R;
-  const unsigned wgs = (unsigned)((g.M + a.rows_per_wg - 1) / a.rows_per_wg);
+  const dim3 wgs((unsigned)((g.M + a.rows_per_wg - 1) / a.rows_per_wg), (unsigned)parts);
   if (U == 1) return R == 1 ? launch<1, 1>(a, wgs, threads, s) : launch<1, 2>(a, wgs, threads, s);
   if (U == 2) return launch<2, 1>(a, wgs, threads, s);
   return launch<4, 1>(a, wgs, threads, s);
