@@ -36,6 +36,11 @@ constexpr int kPagedThreads = 256, kPagedWaves = 4;
 constexpr int kMinUnits = 8;     // least run of a workgroup: 32 keys for each wave
 constexpr int kPartRows = 16;    // query heads of a piece
 
+// Workgroups that share a CU: what the registers of the loads ahead leave (128-long heads
+// with three spill and take twice the time). Heads of 64, 9 sequences with a window of
+// 2048: 18.1 us with two, 17.5 with three, 20.7 with four.
+constexpr int workgroups_per_cu(int head_dim) { return head_dim == 64 ? 3 : 2; }
+
 struct PagedArgs {
   const uint16_t* q;
   const uint8_t* ck;
@@ -46,6 +51,7 @@ struct PagedArgs {
   const int32_t* lengths;
   uint16_t* out;
   float* part;
+  int32_t* sums;
   int64_t ldq, ldo, width, pages;
   int sequences, kv_heads, group, qgroups, page_shift, left, sinks, workgroups;
   float scale_log2;
@@ -72,14 +78,16 @@ __device__ __forceinline__ Span paged_span(const PagedArgs& a, int full) {
   return s;
 }
 
-// Running sums of the sequences' units in LDS (pre[b], b <= sequences), and their total.
-__device__ __forceinline__ int unit_sums(const PagedArgs& a, int* pre, int* waves) {
+// Running sums of the sequences' units in LDS (pre[b], b <= sequences) with their lengths,
+// and the units' total.
+__device__ __forceinline__ int unit_sums(const PagedArgs& a, int* pre, int* len, int* waves) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int before = 0;
   if (tid == 0) pre[0] = 0;
   for (int b0 = 0; b0 < a.sequences; b0 += kPagedThreads) {
     const int b = b0 + tid;
-    int v = b < a.sequences ? paged_span(a, full_length(a, b)).units : 0;
+    const int full = b < a.sequences ? full_length(a, b) : 0;
+    int v = b < a.sequences ? paged_span(a, full).units : 0;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int u = __shfl_up(v, off);
@@ -93,7 +101,10 @@ __device__ __forceinline__ int unit_sums(const PagedArgs& a, int* pre, int* wave
       sum += w < wave ? waves[w] : 0;
       all += waves[w];
     }
-    if (b < a.sequences) pre[b + 1] = sum + v;
+    if (b < a.sequences) {
+      pre[b + 1] = sum + v;
+      len[b] = full;
+    }
     before += all;
     __syncthreads();
   }
@@ -129,7 +140,7 @@ __device__ __forceinline__ uint2 unpack4_mxfp8(uint32_t codes, uint32_t sb) {
 }
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a) {
+__global__ __launch_bounds__(kPagedThreads, workgroups_per_cu(D)) void paged_kernel(const PagedArgs a) {
   constexpr int UNIT = 16 * D * 2;                  // bytes of a unit's values in LDS
   constexpr int LOADS = FP8 ? D / 64 : D / 32;      // 16-byte loads a lane for a unit of keys (or values)
   constexpr int LINE = FP8 ? D : 2 * D;             // bytes of a key in the cache
@@ -139,15 +150,19 @@ __global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a)
   __shared__ float join_ml[kPagedWaves][16][2];
   __shared__ int waves[kPagedWaves];
   int* const pre = reinterpret_cast<int*>(lds + AREA);
+  int* const len = pre + a.sequences + 1;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, g4 = lane >> 4;
-  const int per_seq = unit_sums(a, pre, waves);
+  const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int per_seq = unit_sums(a, pre, len, waves);
   const int64_t total = (int64_t)per_seq * a.kv_heads * a.qgroups;
   const int64_t run = run_units(a, total);
+  __syncthreads();
+  if (blockIdx.x == 0)  // for the second kernel
+    for (int i = tid; i <= a.sequences; i += kPagedThreads) a.sums[i] = pre[i];
   int64_t at = (int64_t)blockIdx.x * run;
   const int64_t stop = min(at + run, total);
   if (at >= stop) return;
-  __syncthreads();
   int h = (int)(at / per_seq);  // key head and group of query heads
   int b;
   {
@@ -171,7 +186,7 @@ __global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a)
     const int u_all = pre[b + 1] - pre[b];
     const int u_last = (int)min((int64_t)u_all, stop - head_at - pre[b]);
     const int hk = h / a.qgroups, qg = h - hk * a.qgroups;
-    const int full = full_length(a, b), n = held_length(a, full);
+    const int full = len[b], n = held_length(a, full);
     const Span span = paged_span(a, full);
     const int lo_key = a.left < 0 ? 0 : full - 1 - a.left;
     const int heads_here = min(kPartRows, a.group - qg * kPartRows);
@@ -192,32 +207,44 @@ __global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a)
     for (int d = 0; d < D / 16; ++d) o[d] = f32x4{0, 0, 0, 0};
     float m = -__builtin_inff(), l = 0.0f;
 
-    for (int u0 = u_first + 2 * wave; u0 < u_last; u0 += 2 * kPagedWaves) {
-      int key[2];
+    // Two units of the wave: their first keys, whether their pages exist, and what the lane
+    // loads of them. The page numbers of a step are read one step before its loads, and the
+    // loads are issued before the arithmetic on the step before.
+    struct Units {
+      int key[2], page[2];
       bool live[2];
       uint4 kr[2][LOADS], vr[2][LOADS];
       uint32_t ksc[2][LOADS], vsc[2][LOADS];
+    };
+    auto look = [&](int u0, Units& x) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int u = min(u0 + i, u_last - 1);
-        key[i] = 16 * (u < span.sink_units ? u : span.first_unit + u - span.sink_units);
-        int page = a.table[(int64_t)b * a.width + (key[i] >> a.page_shift)];
-        live[i] = u0 + i < u_last && (unsigned)page < (uint64_t)a.pages;
-        page = live[i] ? page : 0;
-        const int64_t line = (((int64_t)page * a.kv_heads + hk) << a.page_shift) + (key[i] & ((1 << a.page_shift) - 1));
+        x.key[i] = 16 * (u < span.sink_units ? u : span.first_unit + u - span.sink_units);
+        x.page[i] = a.table[(int64_t)b * a.width + (x.key[i] >> a.page_shift)];
+      }
+    };
+    auto load = [&](int u0, Units& x) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x.live[i] = u0 + i < u_last && (unsigned)x.page[i] < (uint64_t)a.pages;
+        const int page = x.live[i] ? x.page[i] : 0;
+        const int64_t line = (((int64_t)page * a.kv_heads + hk) << a.page_shift) + (x.key[i] & ((1 << a.page_shift) - 1));
         const uint8_t* kb = a.ck + line * LINE;
         const uint8_t* vb = a.cv + line * LINE;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-          kr[i][j] = *reinterpret_cast<const uint4*>(kb + n16 * LINE + 16 * (4 * j + g4));
           const int piece = 64 * j + lane;
-          vr[i][j] = *reinterpret_cast<const uint4*>(vb + piece * 16);
+          x.kr[i][j] = *reinterpret_cast<const uint4*>(kb + n16 * LINE + 16 * (4 * j + g4));
+          x.vr[i][j] = *reinterpret_cast<const uint4*>(vb + piece * 16);
           if constexpr (FP8) {
-            ksc[i][j] = a.cks[(line + n16) * (D / 32) + ((4 * j + g4) >> 1)];
-            vsc[i][j] = a.cvs[(line + piece / CHUNKS) * (D / 32) + ((piece % CHUNKS) >> 1)];
+            x.ksc[i][j] = a.cks[(line + n16) * (D / 32) + ((4 * j + g4) >> 1)];
+            x.vsc[i][j] = a.cvs[(line + piece / CHUNKS) * (D / 32) + ((piece % CHUNKS) >> 1)];
           }
         }
       }
+    };
+    auto attend = [&](const Units& x) {
       f32x4 s[2];
       bool part_unit = false;
 #pragma unroll
@@ -225,25 +252,26 @@ __global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a)
         s[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
+          const uint4 k = x.kr[i][j];
           if constexpr (FP8) {
-            const uint2 x0 = unpack4_mxfp8(kr[i][j].x, ksc[i][j]), x1 = unpack4_mxfp8(kr[i][j].y, ksc[i][j]);
-            const uint2 x2 = unpack4_mxfp8(kr[i][j].z, ksc[i][j]), x3 = unpack4_mxfp8(kr[i][j].w, ksc[i][j]);
+            const uint2 x0 = unpack4_mxfp8(k.x, x.ksc[i][j]), x1 = unpack4_mxfp8(k.y, x.ksc[i][j]);
+            const uint2 x2 = unpack4_mxfp8(k.z, x.ksc[i][j]), x3 = unpack4_mxfp8(k.w, x.ksc[i][j]);
             s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_v, make_uint4(x0.x, x0.y, x1.x, x1.y)),
                                                           qf[2 * j], s[i], 0, 0, 0);
             s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_v, make_uint4(x2.x, x2.y, x3.x, x3.y)),
                                                           qf[2 * j + 1], s[i], 0, 0, 0);
           } else {
-            s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_v, kr[i][j]), qf[j], s[i], 0, 0, 0);
+            s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_v, k), qf[j], s[i], 0, 0, 0);
           }
         }
         // a unit with keys that the query does not see
-        const bool all = live[i] && key[i] + 16 <= n && (key[i] >= lo_key || key[i] + 16 <= a.sinks);
+        const bool all = x.live[i] && x.key[i] + 16 <= n && (x.key[i] >= lo_key || x.key[i] + 16 <= a.sinks);
         part_unit |= !all;
         if (!all) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int k = key[i] + 4 * g4 + r;
-            const bool seen = live[i] && k < n && (k >= lo_key || k < a.sinks);
+            const int k = x.key[i] + 4 * g4 + r;
+            const bool seen = x.live[i] && k < n && (k >= lo_key || k < a.sinks);
             s[i][r] = seen ? s[i][r] : -__builtin_inff();
           }
         }
@@ -255,17 +283,17 @@ __global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a)
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
           const int piece = 64 * j + lane, r = piece / CHUNKS, c = piece % CHUNKS;
-          uint4 v = vr[i][j];
+          const uint4 v = x.vr[i][j];
           uint4 lo = v, hi = v;
           if constexpr (FP8) {
-            const uint2 x0 = unpack4_mxfp8(v.x, vsc[i][j]), x1 = unpack4_mxfp8(v.y, vsc[i][j]);
-            const uint2 x2 = unpack4_mxfp8(v.z, vsc[i][j]), x3 = unpack4_mxfp8(v.w, vsc[i][j]);
+            const uint2 x0 = unpack4_mxfp8(v.x, x.vsc[i][j]), x1 = unpack4_mxfp8(v.y, x.vsc[i][j]);
+            const uint2 x2 = unpack4_mxfp8(v.z, x.vsc[i][j]), x3 = unpack4_mxfp8(v.w, x.vsc[i][j]);
             lo = make_uint4(x0.x, x0.y, x1.x, x1.y);
             hi = make_uint4(x2.x, x2.y, x3.x, x3.y);
           }
           if (part_unit) {
-            const int k = key[i] + r;
-            if (!(live[i] && k < n && (k >= lo_key || k < a.sinks))) lo = hi = make_uint4(0, 0, 0, 0);
+            const int k = x.key[i] + r;
+            if (!(x.live[i] && k < n && (k >= lo_key || k < a.sinks))) lo = hi = make_uint4(0, 0, 0, 0);
           }
           const int swz = D == 128 ? r & 7 : (r >> 1) & 3;
           uint8_t* dst = vlds + i * UNIT + r * D * 2;
@@ -303,6 +331,29 @@ __global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a)
         const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(src + UNIT));
         const bf16x8_v vf = __builtin_bit_cast(bf16x8_v, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8_v, p), o[d], 0, 0, 0);
+      }
+    };
+
+    constexpr int STEP = 2 * kPagedWaves;
+    int u0 = u_first + 2 * wave;
+    if (u0 < u_last) {
+      Units x, y;
+      look(u0, x);
+      look(u0 + STEP, y);  // (past the run: its last unit, not used)
+      load(u0, x);
+      for (;;) {
+        const bool more = u0 + STEP < u_last;
+        if (more) load(u0 + STEP, y);
+        Units z;
+        look(u0 + 2 * STEP, z);
+        attend(x);
+        if (!more) break;
+        u0 += STEP;
+        x = y;
+        y.key[0] = z.key[0];
+        y.key[1] = z.key[1];
+        y.page[0] = z.page[0];
+        y.page[1] = z.page[1];
       }
     }
 
@@ -364,91 +415,88 @@ __global__ __launch_bounds__(kPagedThreads) void paged_kernel(const PagedArgs a)
   }
 }
 
-// Joins the pieces of cut sequences, and writes the zeros of empty ones. One
-// workgroup per sequence and query head: 256 / (D / 4) pieces at a time.
-template <int D>
+// Joins the pieces of cut sequences, and writes the zeros of empty ones. HEADS query heads
+// to a workgroup, the pieces of each over 256 / HEADS / (D / 4) groups of threads.
+template <int D, int HEADS>
 __global__ __launch_bounds__(kPagedThreads) void paged_join_kernel(const PagedArgs a) {
-  constexpr int LANES = D / 4, AHEAD = kPagedThreads / LANES;
-  extern __shared__ __attribute__((aligned(128))) uint8_t lds[];
-  __shared__ __attribute__((aligned(16))) float so[AHEAD][D];
-  __shared__ float sml[AHEAD][2];
-  __shared__ int waves[kPagedWaves];
-  int* const pre = reinterpret_cast<int*>(lds);
-  const int per_seq = unit_sums(a, pre, waves);
+  constexpr int LANES = D / 4, AHEAD = kPagedThreads / HEADS / LANES;
+  __shared__ __attribute__((aligned(16))) float so[HEADS][AHEAD][D];
+  __shared__ float sml[HEADS][AHEAD][2];
   const int heads = a.kv_heads * a.group;
-  const int b = blockIdx.x / heads, head = blockIdx.x % heads;
+  const int mine = threadIdx.x / (LANES * AHEAD);
+  const int lane = threadIdx.x % LANES, which = threadIdx.x / LANES % AHEAD;
+  const int item = min((int)(blockIdx.x * HEADS) + mine, a.sequences * heads - 1);  // (the last one again, past the end)
+  const int b = item / heads, head = item - b * heads;
   const int hk = head / a.group, qg = (head - hk * a.group) / kPartRows;
   const int row = head - hk * a.group - qg * kPartRows;
-  const int lane = threadIdx.x % LANES, which = threadIdx.x / LANES;
   uint16_t* out = a.out + (int64_t)b * a.ldo + (int64_t)head * D + 4 * lane;
-  __syncthreads();
-  const int units = pre[b + 1] - pre[b];
-  if (units == 0) {
-    if (which == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
-    return;
+  const int before = a.sums[b], per_seq = a.sums[a.sequences];
+  const int units = a.sums[b + 1] - before;
+  int64_t i0 = 0, i1 = 0;
+  if (units > 0) {
+    const int64_t run = run_units(a, (int64_t)per_seq * a.kv_heads * a.qgroups);
+    const int64_t f0 = (int64_t)(hk * a.qgroups + qg) * per_seq + before;
+    i0 = f0 / run;
+    i1 = (f0 + units - 1) / run;
   }
-  const int64_t run = run_units(a, (int64_t)per_seq * a.kv_heads * a.qgroups);
-  const int64_t f0 = (int64_t)(hk * a.qgroups + qg) * per_seq + pre[b];
-  const int64_t i0 = f0 / run, i1 = (f0 + units - 1) / run;
-  if (i0 == i1) return;
   const float* ml = a.part + 2 * (int64_t)a.workgroups * kPartRows * D;
   float top = -__builtin_inff(), sum = 0.0f;
   float4 v = make_float4(0, 0, 0, 0);
-  for (int64_t i = i0 + which; i <= i1; i += AHEAD) {
-    const int64_t at = (2 * i + (i == i0 ? 1 : 0)) * kPartRows + row;
-    const float pm = ml[2 * at], pl = ml[2 * at + 1];
-    const float4 x = *reinterpret_cast<const float4*>(a.part + at * D + 4 * lane);
+  auto add = [&](float pm, float pl, const float4& x) {
     const float now = fmaxf(top, pm);
     const float base = now == -__builtin_inff() ? 0.0f : now;
     const float f = __builtin_amdgcn_exp2f(top - base), w = __builtin_amdgcn_exp2f(pm - base);
+    top = now;
     sum = sum * f + pl * w;
     v.x = v.x * f + x.x * w;
     v.y = v.y * f + x.y * w;
     v.z = v.z * f + x.z * w;
     v.w = v.w * f + x.w * w;
-    top = now;
+  };
+  if (i0 < i1)
+#pragma unroll 2
+    for (int64_t i = i0 + which; i <= i1; i += AHEAD) {
+      const int64_t at = (2 * i + (i == i0 ? 1 : 0)) * kPartRows + row;
+      const float2 p = *reinterpret_cast<const float2*>(ml + 2 * at);
+      add(p.x, p.y, *reinterpret_cast<const float4*>(a.part + at * D + 4 * lane));
+    }
+  if constexpr (AHEAD > 1) {
+    *reinterpret_cast<float4*>(&so[mine][which][4 * lane]) = v;
+    if (lane == 0) {
+      sml[mine][which][0] = top;
+      sml[mine][which][1] = sum;
+    }
+    __syncthreads();
+    if (which != 0) return;
+#pragma unroll
+    for (int i = 1; i < AHEAD; ++i) add(sml[mine][i][0], sml[mine][i][1], *reinterpret_cast<const float4*>(&so[mine][i][4 * lane]));
   }
-  *reinterpret_cast<float4*>(&so[which][4 * lane]) = v;
-  if (lane == 0) {
-    sml[which][0] = top;
-    sml[which][1] = sum;
-  }
-  __syncthreads();
-  if (which != 0) return;
-  top = -__builtin_inff();
-  for (int i = 0; i < AHEAD; ++i) top = fmaxf(top, sml[i][0]);
-  const float base = top == -__builtin_inff() ? 0.0f : top;
-  sum = 0.0f;
-  v = make_float4(0, 0, 0, 0);
-  for (int i = 0; i < AHEAD; ++i) {
-    const float w = __builtin_amdgcn_exp2f(sml[i][0] - base);
-    const float4 x = *reinterpret_cast<const float4*>(&so[i][4 * lane]);
-    sum += w * sml[i][1];
-    v.x += w * x.x;
-    v.y += w * x.y;
-    v.z += w * x.z;
-    v.w += w * x.w;
-  }
+  if (units > 0 && i0 == i1) return;  // written by the first kernel
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_rne(v.x * inv, v.y * inv), bf16x2_rne(v.z * inv, v.w * inv));
 }
 
-constexpr int kPagedWorkgroups = 512;
+static int paged_workgroups(int head_dim) { return 256 * workgroups_per_cu(head_dim); }
 
-size_t paged_workspace(const mxq_paged_args&, const mxq_kv_cache& c) {
-  return (size_t)2 * kPagedWorkgroups * kPartRows * (c.head_dim + 2) * 4;
+static size_t part_bytes(int head_dim) { return (size_t)2 * paged_workgroups(head_dim) * kPartRows * (head_dim + 2) * 4; }
+
+size_t paged_workspace(const mxq_paged_args& g, const mxq_kv_cache& c) {
+  return part_bytes(c.head_dim) + (size_t)(g.sequences + 1) * 4;
 }
 
 template <int D>
 static hipError_t launch(const PagedArgs& a, bool fp8, hipStream_t s) {
-  const size_t sums = (size_t)(a.sequences + 1) * 4;
-  const size_t area = kPagedWaves * 16 * D * 4;
+  const size_t bytes = kPagedWaves * 16 * D * 4 + (size_t)(2 * a.sequences + 1) * 4;
   if (fp8)
-    hipLaunchKernelGGL((paged_kernel<D, true>), dim3(a.workgroups), dim3(kPagedThreads), area + sums, s, a);
+    hipLaunchKernelGGL((paged_kernel<D, true>), dim3(a.workgroups), dim3(kPagedThreads), bytes, s, a);
   else
-    hipLaunchKernelGGL((paged_kernel<D, false>), dim3(a.workgroups), dim3(kPagedThreads), area + sums, s, a);
-  hipLaunchKernelGGL((paged_join_kernel<D>), dim3((unsigned)a.sequences * a.kv_heads * a.group), dim3(kPagedThreads), sums, s,
-                     a);
+    hipLaunchKernelGGL((paged_kernel<D, false>), dim3(a.workgroups), dim3(kPagedThreads), bytes, s, a);
+  // few pieces to a sequence: a wave per head
+  const int heads = a.sequences * a.kv_heads * a.group;
+  if (a.sequences * a.kv_heads * a.qgroups * 4 > a.workgroups)
+    hipLaunchKernelGGL((paged_join_kernel<D, 4>), dim3((heads + 3) / 4), dim3(kPagedThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((paged_join_kernel<D, 1>), dim3(heads), dim3(kPagedThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -464,12 +512,13 @@ hipError_t launch_attention_paged(const mxq_paged_args& g, const mxq_kv_cache& c
   a.lengths = g.lengths;
   a.out = static_cast<uint16_t*>(g.out);
   a.part = static_cast<float*>(workspace);
+  a.sums = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + part_bytes(c.head_dim));
   a.ldq = g.ldq; a.ldo = g.ldo; a.width = g.width; a.pages = c.pages;
   a.sequences = (int)g.sequences; a.kv_heads = c.kv_heads; a.group = g.heads / c.kv_heads;
   a.qgroups = (a.group + kPartRows - 1) / kPartRows;
   a.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
   a.left = limit(g.left); a.sinks = limit(g.sinks);
-  a.workgroups = kPagedWorkgroups;
+  a.workgroups = paged_workgroups(c.head_dim);
   a.scale_log2 = g.scale * 1.4426950408889634f;
   return c.head_dim == 128 ? launch<128>(a, c.format == MXQ_KV_MXFP8, s) : launch<64>(a, c.format == MXQ_KV_MXFP8, s);
 }
