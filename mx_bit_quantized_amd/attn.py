@@ -20,7 +20,8 @@ import math
 import torch
 
 from . import _check, lib
-from .block import _index, _on, _ptr, _rows, _same
+from . import block
+from .block import _index, _on, _rows, _same
 
 KV_BF16, KV_MXFP8 = 0, 1
 ROTARY_NORM_NONE, ROTARY_NORM_ROW, ROTARY_NORM_HEAD = 0, 1, 2
@@ -116,6 +117,13 @@ def rotary_frequencies(pairs_per_axis, theta=10000.0, device="cuda"):
     return (torch.tensor(freqs, dtype=torch.float64, device=device), torch.tensor(axis, dtype=torch.int32, device=device))
 
 
+def _ptr(t, name, dev, dtype, shape):
+    """block._ptr, with the usual case in one comparison."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return block._ptr(t, name, dev, dtype, shape)
+
+
 def _heads(t, name, dev, rows=None, heads=None, d=None):
     """(address, row stride) of a bf16 [rows, heads, d] tensor: heads side by side, rows that may be strided."""
     _same(t, name, dev)
@@ -179,15 +187,17 @@ def page_plan(cached, added, block_table, free_pages, page_size, tokens, stream=
         raise ValueError("tokens must not be negative")
     handle, ctx = _on(dev, stream)
     with ctx:
-        # one allocation, cut into parts of a multiple of 16 bytes
-        t4, b4, s4 = -(-tokens // 4) * 4, -(-b // 4) * 4, -(-(b + 1) // 4) * 4
-        buf = torch.empty(2 * t4 + b4 + s4 + 4, dtype=i32, device=cached.device)
-        slots, positions, starts, lengths, taken = buf.split_with_sizes([t4, t4, s4, b4, 4])
+        # one allocation: slots and positions from multiples of 16 bytes on
+        pad = -tokens % 4
+        buf = cached.new_empty(2 * (tokens + pad) + 2 * b + 3)
+        slots, _, positions, _, starts, lengths, taken = buf.split_with_sizes((tokens, pad, tokens, pad, b + 1, b, 2))
         at = buf.data_ptr()
-        st = _lib().mxq_page_plan(pc, pa, pt, pf, b, width, n, page_size, tokens, at, at + 4 * t4, at + 8 * t4,
-                                  at + 8 * t4 + 4 * s4, at + 8 * t4 + 4 * (s4 + b4), handle)
+        pos = at + 4 * (tokens + pad)
+        end = pos + 4 * (tokens + pad)
+        st = _lib().mxq_page_plan(pc, pa, pt, pf, b, width, n, page_size, tokens, at, pos, end, end + 4 * (b + 1),
+                                  end + 4 * (2 * b + 1), handle)
     _check(st, "page_plan")
-    return PagePlan(slots[:tokens], positions[:tokens], starts[:b + 1], lengths[:b], taken[:2])
+    return PagePlan(slots, positions, starts, lengths, taken)
 
 
 def rotary_qkv(qkv, heads, kv_heads, head_dim, positions=None, freqs=None, axis=None, interleaved=False,
@@ -224,8 +234,11 @@ def rotary_qkv(qkv, heads, kv_heads, head_dim, positions=None, freqs=None, axis=
         pax = _ptr(axis, "axis", dev, torch.int32, (pairs,))
     elif positions is not None or axis is not None:
         raise ValueError("positions and axis belong to a rotation (freqs)")
-    of = (lambda n: (n * head_dim,)) if norm == ROTARY_NORM_ROW else (lambda n: (head_dim,))
-    pqw, pkw = _ptr(q_weight, "q_weight", dev, bf16, of(heads)), _ptr(k_weight, "k_weight", dev, bf16, of(kv_heads))
+    pqw = pkw = None
+    if q_weight is not None:
+        pqw = _ptr(q_weight, "q_weight", dev, bf16, (heads * head_dim if norm == ROTARY_NORM_ROW else head_dim,))
+    if k_weight is not None:
+        pkw = _ptr(k_weight, "k_weight", dev, bf16, (kv_heads * head_dim if norm == ROTARY_NORM_ROW else head_dim,))
     if (cache is None) != (slots is None):
         raise ValueError("cache and slots belong together")
     if cache is not None:
@@ -241,14 +254,18 @@ def rotary_qkv(qkv, heads, kv_heads, head_dim, positions=None, freqs=None, axis=
         ldq = ldk = 0
         if heads > 0:
             if q is None:
-                q = torch.empty((m, heads, head_dim), dtype=bf16, device=qkv.device)
-            pq, ldq = _heads(q, "q", dev, m, heads, head_dim)
+                q = qkv.new_empty((m, heads, head_dim))
+                pq, ldq = q.data_ptr(), heads * head_dim
+            else:
+                pq, ldq = _heads(q, "q", dev, m, heads, head_dim)
         elif q is not None:
             raise ValueError("q is an output of a call with heads")
         if kv_heads > 0 and write_k:
             if k is None:
-                k = torch.empty((m, kv_heads, head_dim), dtype=bf16, device=qkv.device)
-            pk, ldk = _heads(k, "k", dev, m, kv_heads, head_dim)
+                k = qkv.new_empty((m, kv_heads, head_dim))
+                pk, ldk = k.data_ptr(), kv_heads * head_dim
+            else:
+                pk, ldk = _heads(k, "k", dev, m, kv_heads, head_dim)
         elif k is not None:
             raise ValueError("k is an output of a call with kv_heads")
         args = RotaryArgs(px, pp, pf, pax, pqw, pkw, pq, pk, ps, m, ldx, ldq, ldk, ld_pos, heads, kv_heads, head_dim, axes, pairs,
@@ -298,7 +315,7 @@ def attention(q, k, v, starts_q=None, starts_k=None, scale=None, window=(-1, -1)
     handle, ctx = _on(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty((mq, heads, d), dtype=torch.bfloat16, device=q.device)
+            out = q.new_empty((mq, heads, d))
             po, ldo = out.data_ptr(), heads * d
         else:
             po, ldo = _heads(out, "out", dev, mq, heads, d)
@@ -336,7 +353,7 @@ def attention_paged(q, cache, block_table, lengths, scale=None, window=-1, sinks
     handle, ctx = _on(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty((b, heads, d), dtype=torch.bfloat16, device=q.device)
+            out = q.new_empty((b, heads, d))
             po, ldo = out.data_ptr(), heads * d
         else:
             po, ldo = _heads(out, "out", dev, b, heads, d)

@@ -4,14 +4,15 @@
 // One launch, no atomics and no wait between workgroups: every workgroup forms
 // the two running sums over the requests (new tokens, new pages) in its LDS for
 // itself, 8 bytes a request from the L2, and then places its own tokens. A
-// token's request is found by bisection in LDS; four consecutive tokens a thread
-// share one search and their stores. A new page begins at a multiple of the page
-// size that is not cached yet, so the token at that position writes the page
-// into the block table: no other place of the table is written, and the one old
-// entry that tokens read (a request's last page, where it is not full) is not.
+// token's request is found by bisection in LDS. A new page begins at a multiple
+// of the page size that is not cached yet, so the token at that position writes
+// the page into the block table: no other place of the table is written, and the
+// one old entry that tokens read (a request's last page, where it is not full) is
+// not.
 //
-// Bound by latency: three dependent loads and the sums, about 8 bytes a token
-// otherwise.
+// Bound by latency: two dependent loads and the sums, about 8 bytes a token
+// otherwise. A token a thread, so that the loads of a step of one token per
+// request are all under way together.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -41,133 +42,120 @@ __device__ __forceinline__ int64_t plan_pages(int64_t n, int shift, int64_t widt
   return p < width ? p : width;
 }
 
-// Inclusive sum over the workgroup; *total gets the last one.
-__device__ __forceinline__ int block_scan(int v, int* waves, int* total) {
+// Inclusive sums of two numbers over the workgroup, and their totals.
+__device__ __forceinline__ void block_scan2(int& a, int& b, int (&waves)[kPlanThreads / 64][2], int& all_a, int& all_b) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int u = __shfl_up(v, off);
-    if (lane >= off) v += u;
+    const int ua = __shfl_up(a, off), ub = __shfl_up(b, off);
+    if (lane >= off) {
+      a += ua;
+      b += ub;
+    }
   }
-  if (lane == 63) waves[wave] = v;
+  if (lane == 63) {
+    waves[wave][0] = a;
+    waves[wave][1] = b;
+  }
   __syncthreads();
-  int before = 0, all = 0;
+  all_a = all_b = 0;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 64; ++w) {
-    before += w < wave ? waves[w] : 0;
-    all += waves[w];
+    a += w < wave ? waves[w][0] : 0;
+    b += w < wave ? waves[w][1] : 0;
+    all_a += waves[w][0];
+    all_b += waves[w][1];
   }
-  __syncthreads();
-  *total = all;
-  return v + before;
 }
 
 __global__ __launch_bounds__(kPlanThreads) void page_plan_kernel(const PlanArgs a) {
-  extern __shared__ int sums[];  // starts [requests + 1], then first new page [requests]
-  __shared__ int waves[kPlanThreads / 64];
+  // per request: first token (and the end), first new page, tokens in the cache
+  extern __shared__ int sums[];
+  __shared__ int waves[kPlanThreads / 64][2];
   int* const first = sums;
-  int* const base = sums + a.requests + 1;
+  int* const base = first + a.requests + 1;
+  int* const cache = base + a.requests;
   const int tid = threadIdx.x;
   const int64_t page = int64_t(1) << a.shift;
 
-  int tokens_before = 0, pages_before = 0, unplaced = 0;
-  for (int r0 = 0; r0 < a.requests; r0 += kPlanThreads) {
-    const int r = r0 + tid;
-    int c = 0, n = 0, have = 0, need = 0;
-    if (r < a.requests) {
-      c = max(a.cached[r], 0);
-      n = max(a.added[r], 0);
-      have = (int)plan_pages(c, a.shift, a.width);
-      need = (int)(plan_pages((int64_t)c + n, a.shift, a.width) - have);
-    }
-    int all_tokens, all_pages;
-    const int t = tokens_before + block_scan(n, waves, &all_tokens);
-    const int p = pages_before + block_scan(need, waves, &all_pages);
-    if (r < a.requests) {
-      first[r + 1] = t;
-      base[r] = p - need;
-      if (blockIdx.x == 0) {
-        a.starts[r + 1] = t;
-        a.lengths[r] = c + n;
-        // tokens on an old page that the table lacks, and those behind the last page it gets
-        const int64_t got = max((int64_t)0, min((int64_t)need, a.n_free - (p - need)));
-        const int64_t end = (have + got) << a.shift;
-        const int64_t old_end = min((int64_t)c + n, (int64_t)have << a.shift);
-        if (old_end > c && a.table[(int64_t)r * a.width + have - 1] < 0) unplaced += (int)(old_end - c);
-        unplaced += (int)max((int64_t)0, (int64_t)c + n - max((int64_t)c, end));
-      }
-    }
-    tokens_before += all_tokens;
-    pages_before += all_pages;
+  // a run of requests per thread
+  const int per = (a.requests + kPlanThreads - 1) / kPlanThreads;
+  const int r_begin = min(tid * per, a.requests), r_end = min(r_begin + per, a.requests);
+  int tokens = 0, pages = 0;
+  for (int r = r_begin; r < r_end; ++r) {
+    const int c = max(a.cached[r], 0), n = max(a.added[r], 0);
+    first[r] = n;
+    cache[r] = c;
+    tokens += n;
+    pages += (int)(plan_pages((int64_t)c + n, a.shift, a.width) - plan_pages(c, a.shift, a.width));
   }
-  if (tid == 0) first[0] = 0;
-  if (blockIdx.x == 0) {
-    int all;
-    block_scan(unplaced, waves, &all);
-    if (tid == 0) {
-      a.starts[0] = 0;
-      a.taken[0] = (int)min((int64_t)pages_before, a.n_free);
-      a.taken[1] = all;
-    }
+  int t = tokens, p = pages, all_tokens, all_pages;
+  block_scan2(t, p, waves, all_tokens, all_pages);
+  t -= tokens;
+  p -= pages;
+  for (int r = r_begin; r < r_end; ++r) {
+    const int c = cache[r], n = first[r];
+    first[r] = t;
+    base[r] = p;
+    t += n;
+    p += (int)(plan_pages((int64_t)c + n, a.shift, a.width) - plan_pages(c, a.shift, a.width));
   }
+  if (tid == 0) first[a.requests] = all_tokens;
   __syncthreads();
 
-  const int64_t live = tokens_before;
+  const int64_t live = all_tokens;
   const int64_t end = live > a.tokens ? live : a.tokens;
-  for (int64_t t0 = 4 * ((int64_t)blockIdx.x * kPlanThreads + tid); t0 < end; t0 += 4 * (int64_t)gridDim.x * kPlanThreads) {
-    int32_t slot[4], pos[4];
-    int r = 0;
-    if (t0 < live) {  // the last request that starts at or before t0
-      int lo = 0, hi = a.requests;
+  for (int64_t at = (int64_t)blockIdx.x * kPlanThreads + tid; at < end; at += (int64_t)gridDim.x * kPlanThreads) {
+    int slot = -1, pos = 0;
+    if (at < live) {
+      int lo = 0, hi = a.requests;  // the last request that starts at or before the token
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (first[mid] <= t0)
+        if (first[mid] <= at)
           lo = mid;
         else
           hi = mid;
       }
-      r = lo;
-    }
-    int64_t c = -1, have = 0;
-    int held = -1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + i;
-      slot[i] = -1;
-      pos[i] = 0;
-      if (t >= live) continue;
-      while (first[r + 1] <= t) {
-        ++r;
-        c = -1;
-      }
-      if (c < 0) {
-        c = max(a.cached[r], 0);
-        have = plan_pages(c, a.shift, a.width);
-        held = (c & (page - 1)) != 0 && have > 0 ? a.table[(int64_t)r * a.width + have - 1] : -1;
-      }
-      const int64_t p = c + (t - first[r]);
-      const int64_t col = p >> a.shift;
-      pos[i] = (int32_t)p;
-      if (col >= a.width) continue;
-      int id = held;
-      if (col >= have) {
-        const int64_t k = base[r] + (col - have);
-        id = k >= 0 && k < a.n_free ? a.free_pages[k] : -1;  // (k < 0: sums past 32 bits)
-        if ((p & (page - 1)) == 0) a.table[(int64_t)r * a.width + col] = id;
-      }
-      if (id >= 0) slot[i] = (int32_t)(((int64_t)id << a.shift) + (p & (page - 1)));
-    }
-    if (t0 + 4 <= a.tokens && ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0) {
-      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t0 + i < a.tokens) {
-          a.slots[t0 + i] = slot[i];
-          a.positions[t0 + i] = pos[i];
+      const int64_t c = cache[lo], q = c + (at - first[lo]), col = q >> a.shift, have = plan_pages(c, a.shift, a.width);
+      pos = (int)q;
+      if (col < a.width) {
+        int id = -1;
+        if (col < have) {
+          id = a.table[(int64_t)lo * a.width + col];
+        } else {
+          const int64_t k = base[lo] + (col - have);
+          id = k >= 0 && k < a.n_free ? a.free_pages[k] : -1;  // (k < 0: sums past 32 bits)
+          if ((q & (page - 1)) == 0) a.table[(int64_t)lo * a.width + col] = id;
         }
+        if (id >= 0) slot = (int)(((int64_t)id << a.shift) + (q & (page - 1)));
+      }
     }
+    if (at < a.tokens) {
+      a.slots[at] = slot;
+      a.positions[at] = pos;
+    }
+  }
+
+  if (blockIdx.x != 0) return;
+  int unplaced = 0;
+  for (int r = tid; r < a.requests; r += kPlanThreads) {
+    const int64_t c = cache[r], n = first[r + 1] - first[r], have = plan_pages(c, a.shift, a.width);
+    const int64_t need = plan_pages(c + n, a.shift, a.width) - have;
+    a.starts[r] = first[r];
+    a.lengths[r] = (int)(c + n);
+    // tokens on an old page that the table lacks, and those behind the last page it gets
+    const int64_t got = max((int64_t)0, min(need, a.n_free - base[r]));
+    const int64_t old_end = min(c + n, have << a.shift), last = (have + got) << a.shift;
+    if (old_end > c && a.table[(int64_t)r * a.width + have - 1] < 0) unplaced += (int)(old_end - c);
+    unplaced += (int)max((int64_t)0, c + n - max(c, last));
+  }
+  __syncthreads();
+  int none = 0, all = 0, zero = 0;
+  block_scan2(unplaced, none, waves, all, zero);
+  if (tid == 0) {
+    a.starts[a.requests] = all_tokens;
+    a.taken[0] = (int)min((int64_t)all_pages, a.n_free);
+    a.taken[1] = all;
   }
 }
 
@@ -177,10 +165,9 @@ hipError_t launch_page_plan(const int32_t* cached, const int32_t* added, int32_t
                             hipStream_t s) {
   const PlanArgs a{cached, added, block_table, free_pages, slots, positions, starts, lengths, taken, tokens, n_free, width,
                    (int)requests, __builtin_ctzll((unsigned long long)page_size)};
-  const int64_t per_wg = 4 * kPlanThreads;
-  const int64_t want = (tokens + per_wg - 1) / per_wg;
+  const int64_t want = (tokens + kPlanThreads - 1) / kPlanThreads;
   const unsigned grid = (unsigned)(want < 1 ? 1 : want > 1024 ? 1024 : want);
-  hipLaunchKernelGGL(page_plan_kernel, dim3(grid), dim3(kPlanThreads), (size_t)(2 * requests + 1) * 4, s, a);
+  hipLaunchKernelGGL(page_plan_kernel, dim3(grid), dim3(kPlanThreads), (size_t)(3 * requests + 1) * 4, s, a);
   return hipGetLastError();
 }
 
