@@ -144,10 +144,11 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // A copy of 16 bytes a lane from a buffer to LDS: lane i's, at byte off, lands at lds + 16 i;
 // past the buffer's end it is zeros. In asm, so that the compiler's waits for it (it would
 // wait for all copies before the next LDS read) stay out of the loop, which waits before its
-// barrier. s_nop: M0 needs one wait state before the copy, a resource five if a vector
-// instruction wrote it (the compiler brings a spilled one back with one).
+// barrier. M0 needs one wait state before the copy. A resource that a vector instruction
+// wrote (the compiler brings spilled ones back so) would need five; none is spilled here, and
+// a test reads the distance off the built code.
 __device__ __forceinline__ void copy16(const i32x4& rs, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(off), "s"(rs) : "memory", "m0");
 }
 __device__ __forceinline__ void tile_barrier() {
@@ -165,8 +166,6 @@ template <int N, class F>
 __device__ __forceinline__ void unroll(F&& f) {
   [&]<int... I>(std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }(std::make_integer_sequence<int, N>{});
 }
-
-constexpr int LEAD = 4;  // fragments of operand A read ahead
 
 template <int D, int QT, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a) {
@@ -194,30 +193,35 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
     koff[c] = (uint32_t)(2 * (r * a.ldk + 8 * k_chunk<D>(r, at)));
     voff[c] = (uint32_t)(2 * (r * a.ldv + 8 * v_chunk<D>(r, at)));
   }
-  auto tile_rows = [&](const uint16_t* base, int64_t ld, int key) {
+  // the rows of tile t; past the last tile nothing (zeros, to a place that is not read any more)
+  auto tile_rows = [&](const uint16_t* base, int64_t ld, int t) {
+    const int key = tile_key(t);
     const uint64_t at = (uint64_t)(base + key * ld);
     const int last = min(nk - key, kKeys) - 1;  // (64 rows of 2^24 elements stay below 2^31 bytes)
     i32x4 r;
     r.x = (int)(uint32_t)at;
     r.y = (int)(uint32_t)(at >> 32) & 0xFFFF;
-    r.z = last * (int)ld * 2 + 2 * D;
+    r.z = t < ntiles ? last * (int)ld * 2 + 2 * D : 0;
     r.w = 0x00020000;
     return r;
   };
-  // (past the last tile it is copied again, to a place that is not read any more)
+  auto copy_k = [&](const i32x4& rs, int c, int buf) { copy16(rs, koff[c], lds0 + buf * 2 * TILE + (wave * COPIES + c) * 1024); };
+  auto copy_v = [&](const i32x4& rs, int c, int buf) {
+    copy16(rs, voff[c], lds0 + buf * 2 * TILE + TILE + (wave * COPIES + c) * 1024);
+  };
   auto fetch_k = [&](int t, int buf) {
-    const i32x4 rs = tile_rows(kbase, a.ldk, tile_key(min(t, ntiles - 1)));
+    const i32x4 rs = tile_rows(kbase, a.ldk, t);
 #pragma unroll
-    for (int c = 0; c < COPIES; ++c) copy16(rs, koff[c], lds0 + buf * 2 * TILE + (wave * COPIES + c) * 1024);
+    for (int c = 0; c < COPIES; ++c) copy_k(rs, c, buf);
   };
   auto fetch_v = [&](int t, int buf) {
-    const i32x4 rs = tile_rows(vbase, a.ldv, tile_key(min(t, ntiles - 1)));
+    const i32x4 rs = tile_rows(vbase, a.ldv, t);
 #pragma unroll
-    for (int c = 0; c < COPIES; ++c) copy16(rs, voff[c], lds0 + buf * 2 * TILE + TILE + (wave * COPIES + c) * 1024);
+    for (int c = 0; c < COPIES; ++c) copy_v(rs, c, buf);
   };
 
-  // The loop takes two steps a turn (scores and buffers change places without moves) and the
-  // last tile's product follows it: an even number of tiles has its first one out of turn.
+  // The loop takes two steps a turn (scores and buffers change places without moves): of an
+  // odd number of steps the first one precedes it.
   const int odd = (ntiles - 1) & 1;
   if (ntiles > 0) {
     fetch_k(0, odd);
@@ -242,11 +246,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
   const int wpb = nk - w.nq + divide(min(wrow + (QT * 32 - 1), w.rows - 1), a.by_group);
 
   f32x16 o[QT][DT];
-  float m[QT], l[QT], sum[QT][2];
+  // per query: the running maximum, what raises it, the exponents' shift that it makes, sums of weights
+  float m[QT], bar[QT], shift[QT], l[QT], sum[QT][2];
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
-    m[i] = -__builtin_inff();
-    l[i] = 0.0f;
+    m[i] = bar[i] = -__builtin_inff();
+    shift[i] = l[i] = 0.0f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -288,42 +293,57 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) x = fmaxf(x, s[i][j][r]);
-      top[i] = other_half_max(x);
+      top[i] = x;
     }
   };
-  // hides what the wave's rows do not see of a tile; false if that is nothing
-  auto hide = [&](f32x16 (&s)[QT][2], int key) {
-    const bool whole = key + kKeys <= nk && (a.right < 0 || key + kKeys - 1 <= (int64_t)wpa + a.right) &&
-                       (a.left < 0 || key >= wpb - a.left || key + kKeys <= a.sinks);
-    if (whole) return false;
+  // the tiles of the window that all of the wave's rows see whole: whole_from .. + whole_count - 1
+  const int whole_key = a.left < 0 ? 0 : max(0, wpb - a.left);
+  const int whole_end = a.right < 0 ? nk : (int)min((int64_t)nk, (int64_t)wpa + a.right + 1);
+  const int whole_from = max((whole_key + kKeys - 1) / kKeys - w.tbeg, 0) + w.nsink - w.t_first;
+  const int whole_count = max(0, (whole_end < 0 ? 0 : whole_end / kKeys) - w.tbeg + w.nsink - w.t_first - whole_from);
+  // hides what the wave's rows do not see of tile t; false if that is nothing
+  auto hide = [&](f32x16 (&s)[QT][2], int t) {
+    if ((unsigned)(t - whole_from) < (unsigned)whole_count) return false;
+    const int key = tile_key(t);
+    int first = key + 4 * half;  // the lane's keys are first + 32 j + 8 (r / 4) + r % 4
+    asm volatile("" : "+v"(first));  // (what follows stays out of the loop's registers)
+    const bool high = key + kKeys > whole_end, low = key < whole_key;
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
-      const int hi = a.right < 0 ? nk - 1 : (int)min((int64_t)nk - 1, (int64_t)pos[i] + a.right);
-      const int lo = a.left < 0 ? 0 : pos[i] - a.left;
-      int first = key + 4 * half;
-      asm volatile("" : "+v"(first));  // (else the 32 sums below are kept in registers over the loop)
+      if (high) {
+        const int last = (a.right < 0 ? nk - 1 : (int)min((int64_t)nk - 1, (int64_t)pos[i] + a.right)) - first;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int at = first + 32 * j + 8 * (r >> 2) + (r & 3);
-          const bool seen = at <= hi && (at >= lo || at < a.sinks);
-          s[i][j][r] = seen ? s[i][j][r] : -__builtin_inff();
-        }
+          for (int r = 0; r < 16; ++r)
+            s[i][j][r] = 32 * j + 8 * (r >> 2) + (r & 3) <= last ? s[i][j][r] : -__builtin_inff();
+      }
+      if (low) {
+        const int begin = pos[i] - a.left - first, sinks = a.sinks - first;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int at = 32 * j + 8 * (r >> 2) + (r & 3);
+            s[i][j][r] = at >= begin || at < sinks ? s[i][j][r] : -__builtin_inff();
+          }
+      }
     }
     return true;
   };
-  // raises the running maximum where the tile's is far above it
+  // raises the running maximum where the tile's is far above it (top: of the lane's keys)
   auto raise = [&](const float (&top)[QT]) {
     bool up = false;
 #pragma unroll
-    for (int i = 0; i < QT; ++i) up |= top[i] > m[i] + a.slack;
+    for (int i = 0; i < QT; ++i) up |= top[i] > bar[i];
     if (!__any(up)) return;
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
-      const float now = fmaxf(top[i], m[i]);
+      const float now = fmaxf(other_half_max(top[i]), m[i]);
       const float alpha = now == m[i] ? 1.0f : __builtin_amdgcn_exp2f((m[i] - now) * a.scale_log2);
       m[i] = now;
+      bar[i] = now + a.slack;
+      shift[i] = now == -__builtin_inff() ? 0.0f : -now * a.scale_log2;
       sum[i][0] *= alpha;
       sum[i][1] *= alpha;
 #pragma unroll
@@ -332,9 +352,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
         for (int r = 0; r < 16; ++r) o[i][d][r] *= alpha;
     }
   };
+
   // operand A of a step: its key fragments (of the next tile), then its value fragments
   constexpr int F1 = 2 * DC, F2 = 4 * DT, F = F1 + F2, SLOTS = F * QT;
-  auto key_fragment = [&](int f, uint32_t buf) { return lds_row(ka[f % DC] + buf + (f / DC) * 32 * D * 2); };
+  // (the two halves of the keys in turn: an MFMA then does not wait for the one right before)
+  auto key_fragment = [&](int f, uint32_t buf) { return lds_row(ka[f / 2] + buf + (f % 2) * 32 * D * 2); };
   auto value_fragment = [&](int f, uint32_t buf) {
     const uint32_t at = va[f % DT] + buf + (f / DT) * 16 * D * 2;
     const s16x4 v0 = lds_columns(at), v1 = lds_columns(at + 8 * D * 2);
@@ -352,7 +374,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
   auto ops_before = [](int slot) constexpr {
     return slot <= W ? slot * OPS_W / W : OPS_W + (slot - W) * OPS_M / (SLOTS - W);
   };
-  float shift[QT];
   float e[2][2], arg[2];
   u32x4_v p[QT][4];
   float top[QT];
@@ -370,7 +391,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
         constexpr int b = k - 1, i = b / 4 % QT;
         if constexpr (what < 6) {
           sum[i][what - 4] += e[b & 1][what - 4];
-          asm volatile("" : "+v"(sum[i][what - 4]));  // (stays here: the compiler would move the sums behind the step)
         } else {
           p[i][b / (4 * QT)][b & 3] = bf16x2_rne(e[b & 1][0], e[b & 1][1]);
         }
@@ -379,51 +399,24 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
       constexpr int k = n - OPS_W, i = k / 16, r = 2 * (k % 16);
       const float x = nxt[i][r >> 4][r & 15], y = nxt[i][(r + 1) >> 4][(r + 1) & 15];
       top[i] = r == 0 ? fmaxf(x, y) : fmaxf(fmaxf(top[i], x), y);
-      asm volatile("" : "+v"(top[i]));
     }
   };
-  static_assert(F % LEAD == 0);  // (fragment n is always ring[n % LEAD])
+  constexpr int LEAD = D == 128 ? 8 : 4;  // fragments of operand A read ahead
+  static_assert(F % LEAD == 0 && LEAD * QT >= 2 * COPIES);  // (fragment n is always ring[n % LEAD])
   bf16x8_v ring[LEAD];
 
   if (ntiles > 0) {
     f32x16 sa[QT][2], sb[QT][2];
-    auto shifts = [&] {
-#pragma unroll
-      for (int i = 0; i < QT; ++i) shift[i] = m[i] == -__builtin_inff() ? 0.0f : -m[i] * a.scale_log2;
-    };
-    auto first_scores = [&](int t, uint32_t buf) {
-      scores(sa, buf);
-      hide(sa, tile_key(t));
-      maxima(sa, top);
-      raise(top);
-    };
-    // a tile's weights and product by themselves
-    auto product = [&](uint32_t buf) {
-      shifts();
-      unroll<OPS_W>([&](auto n) { vector_op(n, sa, sb); });
-      unroll<F2>([&](auto f) {
-        const bf16x8_v vf = value_fragment(f, buf);
-#pragma unroll
-        for (int i = 0; i < QT; ++i)
-          o[i][f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8_v, p[i][f / DT]), o[i][f % DT], 0, 0, 0);
-      });
-    };
 #pragma unroll
     for (int i = 0; i < QT; ++i) sum[i][0] = sum[i][1] = 0.0f;
     tile_barrier();
-    first_scores(0, odd * 2 * TILE);
+    scores(sa, odd * 2 * TILE);
+    hide(sa, 0);
+    maxima(sa, top);
+    raise(top);
     tile_barrier();  // (the first keys are read: their place takes the third tile's)
     fetch_k(2, odd);
     fetch_v(1, odd ^ 1);
-    if (odd) {
-      product(2 * TILE);
-      first_scores(1, 0);
-      tile_barrier();
-      fetch_k(3, 0);
-      fetch_v(2, 1);
-    }
-    unroll<LEAD>([&](auto f) { ring[f] = key_fragment(f, 2 * TILE); });
-
     // Step t: scores of tile t + 1 (nxt) and, from those of tile t (cur), its weights and
     // their product with the values. Each MFMA is followed by its share of the vector work
     // and by the read of the fragment LEAD ahead; LEAD fragments before the end all reads of
@@ -431,7 +424,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
     // further, and the next step's fragments are read.
     auto step = [&](f32x16 (&cur)[QT][2], f32x16 (&nxt)[QT][2], int t, auto par) {
       constexpr uint32_t kbuf = (par ^ 1) * 2 * TILE, vbuf = par * 2 * TILE, next_k = par * 2 * TILE;
-      shifts();
+      i32x4 rk, rv;
       unroll<SLOTS>([&](auto slot) {
         constexpr int f = slot / QT, i = slot % QT;
         if constexpr (f == F - LEAD && i == 0) {
@@ -442,8 +435,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
           f32x16 z;
 #pragma unroll
           for (int r = 0; r < 16; ++r) z[r] = 0.0f;
-          nxt[i][f / DC] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], qf[i][f % DC],
-                                                                   f % DC == 0 ? z : nxt[i][f / DC], 0, 0, 0);
+          nxt[i][f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], qf[i][f / 2], f < 2 ? z : nxt[i][f % 2], 0, 0, 0);
         } else {
           constexpr int g = f - F1;
           o[i][g % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], __builtin_bit_cast(bf16x8_v, p[i][g / DT]),
@@ -459,22 +451,45 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
             ring[f % LEAD] = key_fragment(n - F, next_k);
         }
         constexpr int first = ops_before(slot), last = ops_before(slot + 1);
-        if constexpr (f == F - LEAD && i == QT - 1) fetch_k(t + 3, par ^ 1);
-        if constexpr (f == F - LEAD + 1 && i == QT - 1) fetch_v(t + 2, par);
+        // a copy a slot, from the barrier on
+        constexpr int c = slot - (F - LEAD) * QT;
+        if constexpr (c == 0) rk = tile_rows(kbase, a.ldk, t + 3);
+        if constexpr (c == 1) rv = tile_rows(vbase, a.ldv, t + 2);
+        if constexpr (c >= 0 && c < COPIES) copy_k(rk, c, par ^ 1);
+        if constexpr (c >= COPIES && c < 2 * COPIES) copy_v(rv, c - COPIES, par);
         unroll<last - first>([&](auto n) { vector_op(std::integral_constant<int, first + n>{}, cur, nxt); });
         __builtin_amdgcn_sched_barrier(0);
       });
+      // (used here: the compiler would move sums and maxima behind the branches)
 #pragma unroll
-      for (int i = 0; i < QT; ++i) top[i] = other_half_max(top[i]);
-      if (hide(nxt, tile_key(t + 1))) maxima(nxt, top);
+      for (int i = 0; i < QT; ++i) asm volatile("" : "+v"(top[i]), "+v"(sum[i][0]), "+v"(sum[i][1]));
+      if (hide(nxt, t + 1)) maxima(nxt, top);
       raise(top);
     };
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        sb[i][0] = sa[i][0];
+        sb[i][1] = sa[i][1];
+      }
+      unroll<LEAD>([&](auto f) { ring[f] = key_fragment(f, 0); });
+      step(sb, sa, 0, std::integral_constant<int, 1>{});
+    } else {
+      unroll<LEAD>([&](auto f) { ring[f] = key_fragment(f, 2 * TILE); });
+    }
     for (int t = odd; t < ntiles - 1; t += 2) {
       step(sa, sb, t, std::integral_constant<int, 0>{});
       step(sb, sa, t + 1, std::integral_constant<int, 1>{});
     }
+    // the last tile's weights and product
     tile_barrier();
-    product(0);
+    unroll<OPS_W>([&](auto n) { vector_op(n, sa, sb); });
+    unroll<F2>([&](auto f) {
+      const bf16x8_v vf = value_fragment(f, 0);
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
+        o[i][f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8_v, p[i][f / DT]), o[i][f % DT], 0, 0, 0);
+    });
 #pragma unroll
     for (int i = 0; i < QT; ++i) l[i] = sum[i][0] + sum[i][1];
   }
