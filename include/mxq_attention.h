@@ -159,7 +159,7 @@ int mxq_rotary_qkv(const mxq_rotary_args* args, const mxq_kv_cache* cache, hipSt
  *   starts_q, starts_k  device int32 [sequences + 1], not decreasing, or both null
  *              for one sequence of all rows
  *   scale      positive and finite
- * head_dim 64 or 128; heads a multiple of kv_heads; Mq, Mk below 2^30, and
+ * head_dim 64 or 128; heads a multiple of kv_heads; Mq, Mk below 2^29, and
  * Mq * heads / kv_heads below 2^31 - 256.
  * The workspace (mxq_attention_workspace_bytes; 0: it may be null) joins the parts
  * of a long axis when there are few rows. It belongs to the call until its work is

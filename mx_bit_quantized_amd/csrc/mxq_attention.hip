@@ -155,6 +155,19 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+__device__ __forceinline__ void read_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_word(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) uint32_t*>(at);
+}
+// Two bf16 values, infinities and NaNs replaced by zeros.
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t v) {
+  if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+  if ((v & 0x7F800000u) == 0x7F800000u) v &= 0xFFFFu;
+  return v;
+}
 __device__ __forceinline__ bf16x8_v lds_row(uint32_t at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8_v*>(at);
 }
@@ -248,15 +261,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
   f32x16 o[QT][DT];
   // per query: the running maximum, what raises it, the exponents' shift that it makes, sums of weights
   float m[QT], bar[QT], shift[QT], l[QT], sum[QT][2];
+  auto reset = [&] {
 #pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    m[i] = bar[i] = -__builtin_inff();
-    shift[i] = l[i] = 0.0f;
+    for (int i = 0; i < QT; ++i) {
+      m[i] = bar[i] = -__builtin_inff();
+      shift[i] = l[i] = sum[i][0] = sum[i][1] = 0.0f;
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[i][d][r] = 0.0f;
-  }
+        for (int r = 0; r < 16; ++r) o[i][d][r] = 0.0f;
+    }
+  };
+  reset();
 
   // LDS addresses of the lane's operand reads in buffer 0
   uint32_t ka[DC], va[DT];
@@ -407,8 +423,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
 
   if (ntiles > 0) {
     f32x16 sa[QT][2], sb[QT][2];
-#pragma unroll
-    for (int i = 0; i < QT; ++i) sum[i][0] = sum[i][1] = 0.0f;
     tile_barrier();
     scores(sa, odd * 2 * TILE);
     hide(sa, 0);
@@ -490,6 +504,70 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
       for (int i = 0; i < QT; ++i)
         o[i][f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8_v, p[i][f / DT]), o[i][f % DT], 0, 0, 0);
     });
+
+    // An infinity or a NaN among the values of a tile that some rows see and others do not
+    // reaches all of them, as 0 times it. Where a sum is not finite, once more, tile by tile:
+    // such values are left out of the product and added to the rows that see them.
+    bool spoilt = false;
+    if (a.left >= 0 || a.right >= 0) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        float zero = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) zero = __builtin_fmaf(0.0f, o[i][d][r], zero);
+        spoilt |= zero != 0.0f;  // (NaN)
+      }
+      spoilt = __syncthreads_or(spoilt);
+    }
+    if (spoilt) {
+      reset();
+      for (int t = 0; t < ntiles; ++t) {
+        fetch_k(t, 0);
+        fetch_v(t, 0);
+        tile_barrier();
+        scores(sa, 0);
+        hide(sa, t);
+        maxima(sa, top);
+        raise(top);
+        unroll<OPS_W>([&](auto n) { vector_op(n, sa, sb); });
+        unroll<F2>([&](auto f) {
+          u32x4_v vf = __builtin_bit_cast(u32x4_v, value_fragment(f, 0));
+#pragma unroll
+          for (int h = 0; h < 4; ++h) vf[h] = finite_or_zero(vf[h]);
+#pragma unroll
+          for (int i = 0; i < QT; ++i)
+            o[i][f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_v, vf), __builtin_bit_cast(bf16x8_v, p[i][f / DT]),
+                                                                   o[i][f % DT], 0, 0, 0);
+        });
+        const int key = tile_key(t);
+        for (int r = 0; r < kKeys && key + r < nk; ++r) {
+          const uint32_t at = lds0 + TILE + r * D * 2;
+          const uint32_t mine = lds_word(at + 4 * (lane & (D / 2 - 1)));
+          if (!__any(finite_or_zero(mine) != mine)) continue;
+#pragma unroll
+          for (int i = 0; i < QT; ++i) {
+            const bool seen = (a.right < 0 || key + r <= (int64_t)pos[i] + a.right) &&
+                              (a.left < 0 || key + r >= pos[i] - a.left || key + r < a.sinks);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const int el = 32 * d + 2 * e + 4 * half;  // this lane's four elements
+                const uint32_t from = at + 16 * v_chunk<D>(r, el >> 3) + 2 * (el & 7);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t v = lds_word(from + 4 * h), kept = finite_or_zero(v);
+                  if (seen && (v & 0xFFFFu) != (kept & 0xFFFFu)) o[i][d][e + 2 * h] += as_float(v << 16);
+                  if (seen && (v >> 16) != (kept >> 16)) o[i][d][e + 2 * h + 1] += as_float(v & 0xFFFF0000u);
+                }
+              }
+          }
+        }
+        read_barrier();
+      }
+    }
 #pragma unroll
     for (int i = 0; i < QT; ++i) l[i] = sum[i][0] + sum[i][1];
   }
@@ -631,7 +709,6 @@ static hipError_t launch(const AttnArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_attention(const mxq_attention_args& g, void* workspace, hipStream_t s) {
-  auto limit = [](int64_t v) { return (int)(v < 0 ? -1 : v < (1 << 30) ? v : (1 << 30)); };
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(g.q);
   a.k = static_cast<const uint16_t*>(g.k);
@@ -642,7 +719,10 @@ hipError_t launch_attention(const mxq_attention_args& g, void* workspace, hipStr
   a.part = static_cast<float*>(workspace);
   a.ldq = g.ldq; a.ldk = g.ldk; a.ldv = g.ldv; a.ldo = g.ldo;
   a.sequences = (int)g.sequences; a.Mq = (int)g.Mq; a.Mk = (int)g.Mk;
-  a.left = limit(g.left); a.right = limit(g.right); a.sinks = limit(g.sinks);
+  // (a limit that no position reaches is none)
+  a.left = g.left < 0 || g.left >= g.Mk ? -1 : (int)g.left;
+  a.right = g.right < 0 || g.right >= g.Mq ? -1 : (int)g.right;
+  a.sinks = (int)(g.sinks < g.Mk ? g.sinks : g.Mk);
   a.kv_heads = g.kv_heads; a.group = g.heads / g.kv_heads;
   a.slots = (int)attention_slots(g);
   a.splits = attention_splits(g);

@@ -77,7 +77,7 @@ int check_attention(const mxq_attention_args* args) {
   int st = check_heads(a.heads, a.kv_heads);
   if (st != MXQ_OK) return st;
   if (!positive(a.scale)) return MXQ_ERR_MODE;
-  if (!head_dim_ok(a.head_dim) || a.Mq < 0 || a.Mk < 0 || a.Mq >= kMaxRows || a.Mk >= kMaxRows) return MXQ_ERR_SHAPE;
+  if (!head_dim_ok(a.head_dim) || a.Mq < 0 || a.Mk < 0 || a.Mq >= kMaxRows / 2 || a.Mk >= kMaxRows / 2) return MXQ_ERR_SHAPE;
   if (a.sequences < 0 || a.sequences >= kMaxRows || a.sinks < 0) return MXQ_ERR_SHAPE;
   if ((a.starts_q == nullptr || a.starts_k == nullptr) && a.sequences != 1) return MXQ_ERR_SHAPE;
   const int64_t wq = (int64_t)a.heads * a.head_dim, wk = (int64_t)a.kv_heads * a.head_dim;

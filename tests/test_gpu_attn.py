@@ -375,6 +375,37 @@ def test_attention_large_scores():
     attention_check(out, z, k, v, [(m, m)], -1, -1, 0, d ** -0.5, "equal")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("left, right, sinks, nk", [(-1, 0, 0, 150), (40, 0, 3, 300), (20, 30, 0, 300), (-1, 0, 0, 4100)])
+def test_attention_hidden_places_hold_anything(d, left, right, sinks, nk):
+    """Infinities and NaN among keys and values reach the rows that see them and no others."""
+    nq, heads, kv = 150, 2, 1
+    say("hidden", d, left, right, sinks, nk)
+    g = gen(d)
+    q, k, v = randn(g, nq, heads, d), randn(g, nk, kv, d), randn(g, nk, kv, d)
+    first = nk - nq
+    nan, inf = float("nan"), float("inf")
+    k[nk - 9, 0, 5], k[first + 70, 0, 1] = nan, inf
+    v[nk - 30, 0, 3], v[nk - 31, 0, 4], v[nk - 31, 0, d - 1], v[nk - 7, 0, 17] = nan, inf, -inf, inf
+    v[first + 31, 0, 33] = -inf
+    out = host(mxq.attention(q.to(DEV), k.to(DEV), v.to(DEV), window=(left, right), sinks=sinks))
+    clean = 0
+    for h in range(heads):
+        with np.errstate(all="ignore"):
+            o, mean, top = oracle.attention_rows(host(q)[:, h], host(k)[:, 0], host(v)[:, 0], first, left, right, sinks, d ** -0.5)
+        # a score of +inf leaves no finite weight: the definition's row is NaN
+        for i in range(nq):
+            if np.isnan(o[i]).all():
+                assert np.isnan(out[i, h]).all(), i
+                continue
+            fine = np.isfinite(o[i])
+            clean += fine.all()
+            assert np.array_equal(np.isnan(o[i]), np.isnan(out[i, h])) and np.array_equal(o[i][~fine], out[i, h][~fine], equal_nan=True), i
+            off = (2 * (2 * d + 8 + 4 * (nk // 64 + 2)) * U * top[i] + 2.0 ** -19 + BF) * mean[i][fine]
+            assert (np.abs(out[i, h][fine] - o[i][fine]) <= BF * (np.abs(o[i][fine]) + off) + off).all(), i
+    assert clean > 20
+
+
 # ----------------------------------------------------------------- paged ----
 
 def paged_case(lengths, kv, d, page, fmt, seed, width=None, spare=3):
