@@ -1,7 +1,7 @@
 // mxq_attention.hip - attention of ragged sequences (mxq_attention).
 //
 // One pass over the keys with a running maximum and sum per query. A workgroup
-// holds 32 QT NW rows of one key head and sequence: row R is query R / G, head
+// holds 32 NW rows of one key head and sequence: row R is query R / G, head
 // R % G of the G query heads that share the key head, so that all of them read a
 // key tile once. Tiles of 64 keys and their values go to LDS by asynchronous
 // copies, one tile ahead.
@@ -105,20 +105,26 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lane, Work& w) 
   int tile = slot;
   if (a.starts_q != nullptr) {
     int lo = 0, hi = a.sequences;  // first slot of lo <= slot < that of hi
-    while (hi - lo > 1) {
+    auto first_slot = [&](int b, int s) { return s * a.group / ROWS + b; };
+    while (hi - lo > 64) {
       const int step = (hi - lo + 63) >> 6, probe = lo + lane * step;
       const bool in = probe < hi;
       const int s = in ? min(max(a.starts_q[probe], 0), a.Mq) : 0;
-      const uint64_t ok = __ballot(in && (lane == 0 || s * a.group / ROWS + probe <= slot));
+      const uint64_t ok = __ballot(in && (lane == 0 || first_slot(probe, s) <= slot));
       const int last = 63 - __builtin_clzll(ok | 1);
       hi = min(hi, lo + (last + 1) * step);
       lo += last * step;
     }
-    const int b = __builtin_amdgcn_readfirstlane(lo);
-    w.q0 = min(max(a.starts_q[b], 0), a.Mq);
-    w.nq = min(max(a.starts_q[b + 1], w.q0), a.Mq) - w.q0;
-    w.k0 = min(max(a.starts_k[b], 0), a.Mk);
-    w.nk = min(max(a.starts_k[b + 1], w.k0), a.Mk) - w.k0;
+    // of up to 64 sequences all that is needed, one a lane
+    const int probe = min(lo + lane, hi - 1);
+    const int q0 = min(max(a.starts_q[probe], 0), a.Mq), q1 = min(max(a.starts_q[probe + 1], q0), a.Mq);
+    const int k0 = min(max(a.starts_k[probe], 0), a.Mk), k1 = min(max(a.starts_k[probe + 1], k0), a.Mk);
+    const uint64_t ok = __ballot(lane < hi - lo && (lane == 0 || first_slot(probe, q0) <= slot));
+    const int at = 63 - __builtin_clzll(ok | 1), b = lo + at;
+    w.q0 = __builtin_amdgcn_readlane(q0, at);
+    w.nq = __builtin_amdgcn_readlane(q1, at) - w.q0;
+    w.k0 = __builtin_amdgcn_readlane(k0, at);
+    w.nk = __builtin_amdgcn_readlane(k1, at) - w.k0;
     tile = slot - w.q0 * a.group / ROWS - b;
   }
   w.rows = w.nq * a.group;
@@ -147,9 +153,14 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // barrier. M0 needs one wait state before the copy. A resource that a vector instruction
 // wrote (the compiler brings spilled ones back so) would need five; none is spilled here, and
 // a test reads the distance off the built code.
+template <bool ONCE = false>  // data that is read once leaves the caches to the rest
 __device__ __forceinline__ void copy16(const i32x4& rs, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(off), "s"(rs) : "memory", "m0");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :: "s"(lds), "v"(off), "s"(rs) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(off), "s"(rs) : "memory", "m0");
 }
 __device__ __forceinline__ void tile_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -180,9 +191,9 @@ __device__ __forceinline__ void unroll(F&& f) {
   [&]<int... I>(std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }(std::make_integer_sequence<int, N>{});
 }
 
-template <int D, int QT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a) {
-  constexpr int ROWS = 32 * QT * NW, CH = D / 8, TILE = kKeys * D * 2, DC = D / 16, DT = D / 32;
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, D == 64 ? 3 : 2) void attention_kernel(const AttnArgs a) {
+  constexpr int ROWS = 32 * NW, CH = D / 8, TILE = kKeys * D * 2, DC = D / 16, DT = D / 32;
   constexpr int COPIES = TILE / 1024 / NW;  // of 1 KiB, per wave and tensor
   extern __shared__ __attribute__((aligned(128))) uint8_t lds[];  // [2] of a tile's K, V
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
@@ -236,41 +247,53 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
   // The loop takes two steps a turn (scores and buffers change places without moves): of an
   // odd number of steps the first one precedes it.
   const int odd = (ntiles - 1) & 1;
+
+  // Token, head and position of the lane's row; the place of the wave's first token in q or
+  // out, and how far behind it the lane's row begins, in bytes (32 rows of 2^24 elements).
+  const int wrow = min(w.row0 + wave * 32, w.rows - 1), row = w.row0 + wave * 32 + l32;
+  const int token0 = divide(wrow, a.by_group), token = divide(min(row, w.rows - 1), a.by_group);
+  const int head = min(row, w.rows - 1) - token * a.group, pos = nk - w.nq + token;
+  auto base = [&](int64_t ld) { return (int64_t)(w.q0 + token0) * ld + w.hk * a.group * D; };
+  auto offset = [&](int64_t ld) { return (uint32_t)((token - token0) * (int)ld + head * D) * 2; };
+
+  // The wave's rows of q. With four waves they come as whole rows through LDS, through the
+  // places that the wave itself fills with the second tile (its fragments straight from memory
+  // are 32 bytes of 32 rows at a time); eight waves have no such room, and need it less.
+  constexpr int QPIECES = D / 16;  // of 1 KiB: 64 / CH rows each
+  constexpr bool STAGED = QPIECES == 2 * COPIES;
+  bf16x8_v qf[DC];
+  auto staged = [&](int c) { return lds0 + (odd ^ 1) * 2 * TILE + (c < COPIES ? 0 : TILE - COPIES * 1024) + (wave * COPIES + c) * 1024; };
   if (ntiles > 0) {
+    if constexpr (STAGED) {
+      const uint64_t at = (uint64_t)(a.q + base(a.ldq));
+      const i32x4 rs = {(int)(uint32_t)at, (int)(uint32_t)(at >> 32) & 0xFFFF, 0x7FFFFFFF, 0x00020000};
+#pragma unroll
+      for (int c = 0; c < QPIECES; ++c) {
+        const int r = (c * 64 + lane) / CH;
+        copy16<true>(rs, __shfl(offset(a.ldq), r) + 16 * k_chunk<D>(r, lane % CH), staged(c));
+      }
+    } else {
+      const uint16_t* src = a.q + base(a.ldq) + offset(a.ldq) / 2 + 8 * half;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) qf[c] = *reinterpret_cast<const bf16x8_v*>(src + 16 * c);
+    }
     fetch_k(0, odd);
     fetch_v(0, odd);
-    fetch_k(1, odd ^ 1);
+    if constexpr (!STAGED) fetch_k(1, odd ^ 1);
   }
+  const int wpa = nk - w.nq + token0;  // positions of the wave's first and last row
+  const int wpb = nk - w.nq + divide(min(wrow + 31, w.rows - 1), a.by_group);
 
-  // this wave's rows
-  int pos[QT];
-  bf16x8_v qf[QT][DC];
-#pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    const int r = min(w.row0 + (wave * QT + i) * 32 + l32, w.rows - 1);
-    const int t = divide(r, a.by_group), g = r - t * a.group;
-    pos[i] = nk - w.nq + t;
-    const uint16_t* src = a.q + (int64_t)(w.q0 + t) * a.ldq + (w.hk * a.group + g) * D + 8 * half;
-#pragma unroll
-    for (int c = 0; c < DC; ++c) qf[i][c] = *reinterpret_cast<const bf16x8_v*>(src + 16 * c);
-  }
-  const int wrow = min(w.row0 + wave * QT * 32, w.rows - 1);  // positions of the wave's first and last row
-  const int wpa = nk - w.nq + divide(wrow, a.by_group);
-  const int wpb = nk - w.nq + divide(min(wrow + (QT * 32 - 1), w.rows - 1), a.by_group);
-
-  f32x16 o[QT][DT];
+  f32x16 o[DT];
   // per query: the running maximum, what raises it, the exponents' shift that it makes, sums of weights
-  float m[QT], bar[QT], shift[QT], l[QT], sum[QT][2];
+  float m, bar, shift, l, sum[2];
   auto reset = [&] {
+    m = bar = -__builtin_inff();
+    shift = l = sum[0] = sum[1] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      m[i] = bar[i] = -__builtin_inff();
-      shift[i] = l[i] = sum[i][0] = sum[i][1] = 0.0f;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][d][r] = 0.0f;
-    }
+      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
   };
   reset();
 
@@ -286,31 +309,25 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
   }
 
   // scores of a tile
-  auto scores = [&](f32x16 (&s)[QT][2], uint32_t buf) {
+  auto scores = [&](f32x16 (&s)[2], uint32_t buf) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int c = 0; c < DC; ++c) {
         const bf16x8_v kf = lds_row(ka[c] + buf + j * 32 * D * 2);
+        f32x16 z;
 #pragma unroll
-        for (int i = 0; i < QT; ++i) {
-          f32x16 z;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) z[r] = 0.0f;
-          s[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i][c], c == 0 ? z : s[i][j], 0, 0, 0);
-        }
+        for (int r = 0; r < 16; ++r) z[r] = 0.0f;
+        s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[c], c == 0 ? z : s[j], 0, 0, 0);
       }
   };
-  auto maxima = [&](const f32x16 (&s)[QT][2], float (&top)[QT]) {
+  auto maxima = [&](const f32x16 (&s)[2], float& top) {
+    float x = s[0][0];
 #pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      float x = s[i][0][0];
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x = fmaxf(x, s[i][j][r]);
-      top[i] = x;
-    }
+      for (int r = 0; r < 16; ++r) x = fmaxf(x, s[j][r]);
+    top = x;
   };
   // the tiles of the window that all of the wave's rows see whole: whole_from .. + whole_count - 1
   const int whole_key = a.left < 0 ? 0 : max(0, wpb - a.left);
@@ -318,59 +335,50 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
   const int whole_from = max((whole_key + kKeys - 1) / kKeys - w.tbeg, 0) + w.nsink - w.t_first;
   const int whole_count = max(0, (whole_end < 0 ? 0 : whole_end / kKeys) - w.tbeg + w.nsink - w.t_first - whole_from);
   // hides what the wave's rows do not see of tile t; false if that is nothing
-  auto hide = [&](f32x16 (&s)[QT][2], int t) {
+  auto hide = [&](f32x16 (&s)[2], int t) {
     if ((unsigned)(t - whole_from) < (unsigned)whole_count) return false;
     const int key = tile_key(t);
     int first = key + 4 * half;  // the lane's keys are first + 32 j + 8 (r / 4) + r % 4
     asm volatile("" : "+v"(first));  // (what follows stays out of the loop's registers)
     const bool high = key + kKeys > whole_end, low = key < whole_key;
+    if (high) {
+      const int last = (a.right < 0 ? nk - 1 : (int)min((int64_t)nk - 1, (int64_t)pos + a.right)) - first;
 #pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      if (high) {
-        const int last = (a.right < 0 ? nk - 1 : (int)min((int64_t)nk - 1, (int64_t)pos[i] + a.right)) - first;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int r = 0; r < 16; ++r)
+          s[j][r] = 32 * j + 8 * (r >> 2) + (r & 3) <= last ? s[j][r] : -__builtin_inff();
+    }
+    if (low) {
+      const int begin = pos - a.left - first, sinks = a.sinks - first;
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            s[i][j][r] = 32 * j + 8 * (r >> 2) + (r & 3) <= last ? s[i][j][r] : -__builtin_inff();
-      }
-      if (low) {
-        const int begin = pos[i] - a.left - first, sinks = a.sinks - first;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int at = 32 * j + 8 * (r >> 2) + (r & 3);
-            s[i][j][r] = at >= begin || at < sinks ? s[i][j][r] : -__builtin_inff();
-          }
-      }
+        for (int r = 0; r < 16; ++r) {
+          const int at = 32 * j + 8 * (r >> 2) + (r & 3);
+          s[j][r] = at >= begin || at < sinks ? s[j][r] : -__builtin_inff();
+        }
     }
     return true;
   };
   // raises the running maximum where the tile's is far above it (top: of the lane's keys)
-  auto raise = [&](const float (&top)[QT]) {
-    bool up = false;
+  auto raise = [&](float top) {
+    if (!__any(top > bar)) return;
+    const float now = fmaxf(other_half_max(top), m);
+    const float alpha = now == m ? 1.0f : __builtin_amdgcn_exp2f((m - now) * a.scale_log2);
+    m = now;
+    bar = now + a.slack;
+    shift = now == -__builtin_inff() ? 0.0f : -now * a.scale_log2;
+    sum[0] *= alpha;
+    sum[1] *= alpha;
 #pragma unroll
-    for (int i = 0; i < QT; ++i) up |= top[i] > bar[i];
-    if (!__any(up)) return;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      const float now = fmaxf(other_half_max(top[i]), m[i]);
-      const float alpha = now == m[i] ? 1.0f : __builtin_amdgcn_exp2f((m[i] - now) * a.scale_log2);
-      m[i] = now;
-      bar[i] = now + a.slack;
-      shift[i] = now == -__builtin_inff() ? 0.0f : -now * a.scale_log2;
-      sum[i][0] *= alpha;
-      sum[i][1] *= alpha;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][d][r] *= alpha;
-    }
+      for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
   };
 
   // operand A of a step: its key fragments (of the next tile), then its value fragments
-  constexpr int F1 = 2 * DC, F2 = 4 * DT, F = F1 + F2, SLOTS = F * QT;
+  constexpr int F1 = 2 * DC, F2 = 4 * DT, F = F1 + F2;
   // (the two halves of the keys in turn: an MFMA then does not wait for the one right before)
   auto key_fragment = [&](int f, uint32_t buf) { return lds_row(ka[f / 2] + buf + (f % 2) * 32 * D * 2); };
   auto value_fragment = [&](int f, uint32_t buf) {
@@ -381,49 +389,55 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
   // vector work of a step, instruction by instruction: per pair of scores the exponents'
   // arguments, the weights, and (of the pair before) their sums and bf16 values; then the
   // maxima of the next tile's scores
-  constexpr int PER_PAIR = 7, PAIRS = 16 * QT, OPS_W = PER_PAIR * (PAIRS + 1), OPS_M = 16 * QT;
+  constexpr int PER_PAIR = 7, PAIRS = 16, OPS_W = PER_PAIR * (PAIRS + 1), OPS_M = 16;
   // the weights of the last 16 keys are needed in slot W: all weights come before it,
   // evenly, and the maxima after them
-  constexpr int W = (F1 + 3 * DT) * QT;
-  static_assert(PER_PAIR * (12 * QT + 1) * W < (F1 + 2 * DT) * QT * OPS_W && PER_PAIR * (8 * QT + 1) * W < (F1 + DT) * QT * OPS_W &&
-                PER_PAIR * (4 * QT + 1) * W < F1 * QT * OPS_W);
+  constexpr int W = F1 + 3 * DT;
+  static_assert(PER_PAIR * 13 * W < (F1 + 2 * DT) * OPS_W && PER_PAIR * 9 * W < (F1 + DT) * OPS_W && PER_PAIR * 5 * W < F1 * OPS_W);
   auto ops_before = [](int slot) constexpr {
-    return slot <= W ? slot * OPS_W / W : OPS_W + (slot - W) * OPS_M / (SLOTS - W);
+    return slot <= W ? slot * OPS_W / W : OPS_W + (slot - W) * OPS_M / (F - W);
   };
   float e[2][2], arg[2];
-  u32x4_v p[QT][4];
-  float top[QT];
-  auto vector_op = [&](auto op, f32x16 (&cur)[QT][2], f32x16 (&nxt)[QT][2]) {
+  u32x4_v p[4];
+  float top;
+  auto vector_op = [&](auto op, f32x16 (&cur)[2], f32x16 (&nxt)[2]) {
     constexpr int n = op;
     if constexpr (n < OPS_W) {
       constexpr int k = n / PER_PAIR, what = n % PER_PAIR;
       if constexpr (what < 4 && k < PAIRS) {
-        constexpr int jc = k / (4 * QT), i = k / 4 % QT, r = 8 * (jc & 1) + 2 * (k & 3) + (what & 1);
+        constexpr int jc = k / 4, r = 8 * (jc & 1) + 2 * (k & 3) + (what & 1);
         if constexpr (what < 2)
-          arg[what] = __builtin_fmaf(cur[i][jc >> 1][r], a.scale_log2, shift[i]);
+          arg[what] = __builtin_fmaf(cur[jc >> 1][r], a.scale_log2, shift);
         else
           e[k & 1][what & 1] = __builtin_amdgcn_exp2f(arg[what & 1]);
       } else if constexpr (what >= 4 && k > 0) {
-        constexpr int b = k - 1, i = b / 4 % QT;
+        constexpr int b = k - 1;
         if constexpr (what < 6) {
-          sum[i][what - 4] += e[b & 1][what - 4];
+          sum[what - 4] += e[b & 1][what - 4];
         } else {
-          p[i][b / (4 * QT)][b & 3] = bf16x2_rne(e[b & 1][0], e[b & 1][1]);
+          p[b / 4][b & 3] = bf16x2_rne(e[b & 1][0], e[b & 1][1]);
         }
       }
     } else {
-      constexpr int k = n - OPS_W, i = k / 16, r = 2 * (k % 16);
-      const float x = nxt[i][r >> 4][r & 15], y = nxt[i][(r + 1) >> 4][(r + 1) & 15];
-      top[i] = r == 0 ? fmaxf(x, y) : fmaxf(fmaxf(top[i], x), y);
+      constexpr int r = 2 * (n - OPS_W);
+      const float x = nxt[r >> 4][r & 15], y = nxt[(r + 1) >> 4][(r + 1) & 15];
+      top = r == 0 ? fmaxf(x, y) : fmaxf(fmaxf(top, x), y);
     }
   };
   constexpr int LEAD = D == 128 ? 8 : 4;  // fragments of operand A read ahead
-  static_assert(F % LEAD == 0 && LEAD * QT >= 2 * COPIES);  // (fragment n is always ring[n % LEAD])
+  static_assert(F % LEAD == 0 && LEAD >= 2 * COPIES);  // (fragment n is always ring[n % LEAD])
   bf16x8_v ring[LEAD];
 
   if (ntiles > 0) {
-    f32x16 sa[QT][2], sb[QT][2];
+    f32x16 sa[2], sb[2];
     tile_barrier();
+    if constexpr (STAGED) {
+      const uint32_t mine = staged(l32 * CH / 64) + l32 * CH % 64 * 16;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) qf[c] = lds_row(mine + 16 * k_chunk<D>(l32, 2 * c + half));
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      fetch_k(1, odd ^ 1);
+    }
     scores(sa, odd * 2 * TILE);
     hide(sa, 0);
     maxima(sa, top);
@@ -436,12 +450,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
     // and by the read of the fragment LEAD ahead; LEAD fragments before the end all reads of
     // the step are done and the workgroup meets: the step's tiles give way to those two
     // further, and the next step's fragments are read.
-    auto step = [&](f32x16 (&cur)[QT][2], f32x16 (&nxt)[QT][2], int t, auto par) {
+    auto step = [&](f32x16 (&cur)[2], f32x16 (&nxt)[2], int t, auto par) {
       constexpr uint32_t kbuf = (par ^ 1) * 2 * TILE, vbuf = par * 2 * TILE, next_k = par * 2 * TILE;
       i32x4 rk, rv;
-      unroll<SLOTS>([&](auto slot) {
-        constexpr int f = slot / QT, i = slot % QT;
-        if constexpr (f == F - LEAD && i == 0) {
+      unroll<F>([&](auto slot) {
+        constexpr int f = slot;  // a fragment a slot
+        if constexpr (f == F - LEAD) {
           tile_barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -449,24 +463,21 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
           f32x16 z;
 #pragma unroll
           for (int r = 0; r < 16; ++r) z[r] = 0.0f;
-          nxt[i][f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], qf[i][f / 2], f < 2 ? z : nxt[i][f % 2], 0, 0, 0);
+          nxt[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], qf[f / 2], f < 2 ? z : nxt[f % 2], 0, 0, 0);
         } else {
           constexpr int g = f - F1;
-          o[i][g % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], __builtin_bit_cast(bf16x8_v, p[i][g / DT]),
-                                                                 o[i][g % DT], 0, 0, 0);
+          o[g % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % LEAD], __builtin_bit_cast(bf16x8_v, p[g / DT]), o[g % DT], 0, 0, 0);
         }
-        if constexpr (i == QT - 1) {
-          constexpr int n = f + LEAD;
-          if constexpr (n < F1)
-            ring[f % LEAD] = key_fragment(n, kbuf);
-          else if constexpr (n < F)
-            ring[f % LEAD] = value_fragment(n - F1, vbuf);
-          else
-            ring[f % LEAD] = key_fragment(n - F, next_k);
-        }
-        constexpr int first = ops_before(slot), last = ops_before(slot + 1);
+        constexpr int ahead = f + LEAD;
+        if constexpr (ahead < F1)
+          ring[f % LEAD] = key_fragment(ahead, kbuf);
+        else if constexpr (ahead < F)
+          ring[f % LEAD] = value_fragment(ahead - F1, vbuf);
+        else
+          ring[f % LEAD] = key_fragment(ahead - F, next_k);
+        constexpr int first = ops_before(f), last = ops_before(f + 1);
         // a copy a slot, from the barrier on
-        constexpr int c = slot - (F - LEAD) * QT;
+        constexpr int c = f - (F - LEAD);
         if constexpr (c == 0) rk = tile_rows(kbase, a.ldk, t + 3);
         if constexpr (c == 1) rv = tile_rows(vbase, a.ldv, t + 2);
         if constexpr (c >= 0 && c < COPIES) copy_k(rk, c, par ^ 1);
@@ -475,17 +486,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
         __builtin_amdgcn_sched_barrier(0);
       });
       // (used here: the compiler would move sums and maxima behind the branches)
-#pragma unroll
-      for (int i = 0; i < QT; ++i) asm volatile("" : "+v"(top[i]), "+v"(sum[i][0]), "+v"(sum[i][1]));
+      asm volatile("" : "+v"(top), "+v"(sum[0]), "+v"(sum[1]));
       if (hide(nxt, t + 1)) maxima(nxt, top);
       raise(top);
     };
     if (odd) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        sb[i][0] = sa[i][0];
-        sb[i][1] = sa[i][1];
-      }
+      sb[0] = sa[0];
+      sb[1] = sa[1];
       unroll<LEAD>([&](auto f) { ring[f] = key_fragment(f, 0); });
       step(sb, sa, 0, std::integral_constant<int, 1>{});
     } else {
@@ -500,9 +507,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
     unroll<OPS_W>([&](auto n) { vector_op(n, sa, sb); });
     unroll<F2>([&](auto f) {
       const bf16x8_v vf = value_fragment(f, 0);
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        o[i][f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8_v, p[i][f / DT]), o[i][f % DT], 0, 0, 0);
+      o[f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, __builtin_bit_cast(bf16x8_v, p[f / DT]), o[f % DT], 0, 0, 0);
     });
 
     // An infinity or a NaN among the values of a tile that some rows see and others do not
@@ -510,16 +515,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
     // such values are left out of the product and added to the rows that see them.
     bool spoilt = false;
     if (a.left >= 0 || a.right >= 0) {
+      float zero = 0.0f;
 #pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        float zero = 0.0f;
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) zero = __builtin_fmaf(0.0f, o[i][d][r], zero);
-        spoilt |= zero != 0.0f;  // (NaN)
-      }
-      spoilt = __syncthreads_or(spoilt);
+        for (int r = 0; r < 16; ++r) zero = __builtin_fmaf(0.0f, o[d][r], zero);
+      spoilt = __syncthreads_or(zero != 0.0f);  // (NaN)
     }
     if (spoilt) {
       reset();
@@ -536,77 +537,71 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_kernel(const AttnArgs a)
           u32x4_v vf = __builtin_bit_cast(u32x4_v, value_fragment(f, 0));
 #pragma unroll
           for (int h = 0; h < 4; ++h) vf[h] = finite_or_zero(vf[h]);
-#pragma unroll
-          for (int i = 0; i < QT; ++i)
-            o[i][f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_v, vf), __builtin_bit_cast(bf16x8_v, p[i][f / DT]),
-                                                                   o[i][f % DT], 0, 0, 0);
+          o[f % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_v, vf), __builtin_bit_cast(bf16x8_v, p[f / DT]),
+                                                              o[f % DT], 0, 0, 0);
         });
         const int key = tile_key(t);
         for (int r = 0; r < kKeys && key + r < nk; ++r) {
           const uint32_t at = lds0 + TILE + r * D * 2;
           const uint32_t mine = lds_word(at + 4 * (lane & (D / 2 - 1)));
           if (!__any(finite_or_zero(mine) != mine)) continue;
+          const bool seen = (a.right < 0 || key + r <= (int64_t)pos + a.right) &&
+                            (a.left < 0 || key + r >= pos - a.left || key + r < a.sinks);
 #pragma unroll
-          for (int i = 0; i < QT; ++i) {
-            const bool seen = (a.right < 0 || key + r <= (int64_t)pos[i] + a.right) &&
-                              (a.left < 0 || key + r >= pos[i] - a.left || key + r < a.sinks);
+          for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
+            for (int e = 0; e < 16; e += 4) {
+              const int el = 32 * d + 2 * e + 4 * half;  // this lane's four elements
+              const uint32_t from = at + 16 * v_chunk<D>(r, el >> 3) + 2 * (el & 7);
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const int el = 32 * d + 2 * e + 4 * half;  // this lane's four elements
-                const uint32_t from = at + 16 * v_chunk<D>(r, el >> 3) + 2 * (el & 7);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t v = lds_word(from + 4 * h), kept = finite_or_zero(v);
-                  if (seen && (v & 0xFFFFu) != (kept & 0xFFFFu)) o[i][d][e + 2 * h] += as_float(v << 16);
-                  if (seen && (v >> 16) != (kept >> 16)) o[i][d][e + 2 * h + 1] += as_float(v & 0xFFFF0000u);
-                }
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t v = lds_word(from + 4 * h), kept = finite_or_zero(v);
+                if (seen && (v & 0xFFFFu) != (kept & 0xFFFFu)) o[d][e + 2 * h] += as_float(v << 16);
+                if (seen && (v >> 16) != (kept >> 16)) o[d][e + 2 * h + 1] += as_float(v & 0xFFFF0000u);
               }
-          }
+            }
         }
         read_barrier();
       }
     }
-#pragma unroll
-    for (int i = 0; i < QT; ++i) l[i] = sum[i][0] + sum[i][1];
+    l = sum[0] + sum[1];
   }
 
+  if constexpr (NW != 4) read_barrier();  // (the last values are read: rows take their place)
+  l = other_half_sum(l);
+  if (a.splits > 1) {
+    if (row >= w.rows) return;
+    // unnormalised part: D sums, the maximum (in units of log2) and the sum of weights
+    const int64_t at = ((int64_t)w.split * a.Mq + w.q0 + token) * (a.kv_heads * a.group) + w.hk * a.group + head;
+    float* dst = a.part + at * D;
 #pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    l[i] = other_half_sum(l[i]);
-    const int row = w.row0 + (wave * QT + i) * 32 + l32;
-    const int t = divide(min(row, w.rows - 1), a.by_group), g = row - t * a.group;
-    if (a.splits > 1) {
-      if (row >= w.rows) continue;
-      // unnormalised part: D sums, the maximum (in units of log2) and the sum of weights
-      const int64_t at = ((int64_t)w.split * a.Mq + w.q0 + t) * (a.kv_heads * a.group) + w.hk * a.group + g;
-      float* dst = a.part + at * D;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4*>(dst + 32 * d + 2 * r + 4 * half) = make_float4(o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]);
+    if (half == 0) {
+      float* ml = a.part + (int64_t)a.splits * a.Mq * (a.kv_heads * a.group) * D + 2 * at;
+      ml[0] = m * a.scale_log2;
+      ml[1] = l;
+    }
+  } else {
+    // through LDS, so that rows leave whole: 8 bytes a lane in, 16 bytes a lane out, chunks
+    // permuted like those of K
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const uint32_t mine = lds0 + (NW == 4 ? 2 * TILE : 0) + wave * 64 * D;
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          *reinterpret_cast<float4*>(dst + 32 * d + 2 * r + 4 * half) = make_float4(o[i][d][r], o[i][d][r + 1], o[i][d][r + 2], o[i][d][r + 3]);
-      if (half == 0) {
-        float* ml = a.part + (int64_t)a.splits * a.Mq * (a.kv_heads * a.group) * D + 2 * at;
-        ml[0] = m[i] * a.scale_log2;
-        ml[1] = l[i];
-      }
-    } else {
-      const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-      uint16_t* dst = a.out + (int64_t)(w.q0 + t) * a.ldo + (w.hk * a.group + g) * D + 8 * half;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<__attribute__((address_space(3))) u32x2_v*>(mine + l32 * D * 2 + 16 * k_chunk<D>(l32, 4 * d + r / 4) + 8 * half) =
+            u32x2_v{bf16x2_rne(o[d][r] * inv, o[d][r + 1] * inv), bf16x2_rne(o[d][r + 2] * inv, o[d][r + 3] * inv)};
 #pragma unroll
-        for (int r = 0; r < 16; r += 8) {
-          // elements 8 half .. + 7 of 16: the halves' second and first four change places
-          uint32_t x[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) x[h] = bf16x2_rne(o[i][d][r + 2 * h] * inv, o[i][d][r + 2 * h + 1] * inv);
-          const u32x2_v y0 = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
-          const u32x2_v y1 = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
-          if (row < w.rows) *reinterpret_cast<uint4*>(dst + 32 * d + 2 * r) = make_uint4(y0[0], y1[0], y0[1], y1[1]);
-        }
+    for (int n = 0; n < CH / 2; ++n) {
+      const int r = (n * 64 + lane) / CH, ch = lane % CH;
+      const bf16x8_v y = lds_row(mine + r * D * 2 + 16 * k_chunk<D>(r, ch));
+      const uint32_t off = __shfl(offset(a.ldo), r) / 2;
+      if (w.row0 + wave * 32 + r < w.rows)
+        __builtin_nontemporal_store(y, reinterpret_cast<bf16x8_v*>(a.out + base(a.ldo) + off + 8 * ch));
     }
   }
 }
@@ -700,7 +695,7 @@ bool attention_fits(const mxq_attention_args& g) {
 
 template <int D, int NW>
 static hipError_t launch(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attention_kernel<D, 1, NW>), dim3((unsigned)((a.items + 7) / 8 * 8)), dim3(64 * NW), 4 * kKeys * D * 2, s, a);
+  hipLaunchKernelGGL((attention_kernel<D, NW>), dim3((unsigned)((a.items + 7) / 8 * 8)), dim3(64 * NW), 4 * kKeys * D * 2, s, a);
   if (a.splits > 1) {
     const int64_t rows = (int64_t)a.Mq * a.kv_heads * a.group, per = 256 / (D / 4) / kJoin;
     hipLaunchKernelGGL((attention_join_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a);
