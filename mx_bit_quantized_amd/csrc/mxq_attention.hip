@@ -1,10 +1,16 @@
 // mxq_attention.hip - attention of ragged sequences (mxq_attention).
 //
-// One pass over the keys with a running maximum and sum per query. A workgroup
-// holds 32 NW rows of one key head and sequence: row R is query R / G, head
-// R % G of the G query heads that share the key head, so that all of them read a
-// key tile once. Tiles of 64 keys and their values go to LDS by asynchronous
-// copies, one tile ahead.
+// One pass over the keys with a running maximum m and sum l per query:
+//   m' = max(m, max_j s_j), l' = l 2^(m - m') + sum_j 2^(s_j - m'),
+//   o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j, out = o / l,
+// s in units of log2. Scores, m, l and o are fp32; the weights 2^(s - m') are
+// rounded to bf16 for the second product (the sum takes them unrounded), and out
+// once: a relative error of .0020 to .0024 against 64 bits, .0017 of it out's own.
+//
+// A workgroup holds 32 NW rows of one key head and sequence: row R is query R / G,
+// head R % G of the G query heads that share the key head, so that all of them read
+// a key tile once. Tiles of 64 keys and their values go to LDS by asynchronous
+// copies, one to two tiles ahead, double-buffered.
 //
 // Both products are 32x32x16 bf16 MFMAs on transposed operands: S^T = K Q^T puts a
 // query's scores into one lane (and the lane 32 further), so that its maximum and
@@ -12,6 +18,30 @@
 // operand B of O^T = V^T P^T without a move between lanes: the product may take
 // the keys in any order, and the transposing LDS reads of V take them in the order
 // that the scores are held in.
+//
+// A wave issues MFMAs and vector instructions one after the other, and the two
+// pipes work side by side only if they alternate. So a step takes the scores of
+// tile t + 1 and, slot by slot between their MFMAs and those of O, the exponentials,
+// sums, packing and maxima of tile t, fixed in place by scheduling barriers; operand
+// A is read from LDS eight fragments ahead, and a step has one barrier.
+//
+// 32760 x 32760, 40 heads of 128: 17.1 to 18 ms by the card, 1.22 to 1.29 PFLOP/s,
+// against 1.41 to 1.65 PFLOP/s of large library products. There the MFMAs are busy
+// 73% of the cycles and the power cap holds the clock at 1.6 GHz (all-zero operands:
+// 12.95 ms). 65520 queries against 741 keys (6.5 tiles a workgroup): 667 us,
+// 0.83 PFLOP/s; of a workgroup's 28000 cycles 15500 are steps, 5700 the first
+// loads (rows of q from HBM, as the output's on their way there: 2.0 TB/s), 3300 the
+// first scores and the last product without their counterparts, 2800 the way out.
+// Causal prompts with a window of 1024: 330 us, 0.88 PFLOP/s, the same ends and the
+// tiles that the window cuts (a fifth of them). Heads of 64, 296 rows, 30011 keys:
+// 37 us, 0.49 PFLOP/s: as many exponentials for half the products, 23% of the last
+// tile's rows empty, and the join (5 us).
+//
+// Slower, and not kept (before against after, in us or ms): two query tiles a wave at
+// one wave per SIMD 17.5, 22 ms; the sum from the rounded weights by dot products
+// 17.5, 18.2 ms; workgroups that stay and take the next tile 1% faster in the text
+// case, 4% slower with the window; rows of q brought to the L2 by the workgroup
+// before 667, 690; key heads in turn instead of one after the other 692, 699.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -152,8 +182,10 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // wait for all copies before the next LDS read) stay out of the loop, which waits before its
 // barrier. M0 needs one wait state before the copy. A resource that a vector instruction
 // wrote (the compiler brings spilled ones back so) would need five; none is spilled here, and
-// a test reads the distance off the built code.
-template <bool ONCE = false>  // data that is read once leaves the caches to the rest
+// a test reads the distance off the built code. ONCE: data that is read once leaves the caches
+// to the rest (q so, and out stored so: 15 MB of keys and values, 1.3 GB of q and out, 691 us without
+// and 676 with).
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16(const i32x4& rs, uint32_t off, uint32_t lds) {
   if constexpr (ONCE)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
@@ -191,6 +223,7 @@ __device__ __forceinline__ void unroll(F&& f) {
   [&]<int... I>(std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }(std::make_integer_sequence<int, N>{});
 }
 
+// (heads of 64: three workgroups on a CU where there are as many)
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : 2) void attention_kernel(const AttnArgs a) {
   constexpr int ROWS = 32 * NW, CH = D / 8, TILE = kKeys * D * 2, DC = D / 16, DT = D / 32;
@@ -258,7 +291,8 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : 2) void attention_kernel(con
 
   // The wave's rows of q. With four waves they come as whole rows through LDS, through the
   // places that the wave itself fills with the second tile (its fragments straight from memory
-  // are 32 bytes of 32 rows at a time); eight waves have no such room, and need it less.
+  // are 32 bytes of 32 rows at a time: with the way out through LDS 695 us, 682 so, for 65520
+  // queries and 741 keys); eight waves have no such room, and a longer run to spread it over.
   constexpr int QPIECES = D / 16;  // of 1 KiB: 64 / CH rows each
   constexpr bool STAGED = QPIECES == 2 * COPIES;
   bf16x8_v qf[DC];
@@ -657,29 +691,43 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs a) {
       make_uint2(bf16x2_rne(o.x * inv, o.y * inv), bf16x2_rne(o.z * inv, o.w * inv));
 }
 
-// Workgroups of four waves and 128 rows, two on a CU, which fill each other's waits; of
-// eight waves and 256 rows (a key tile is copied half as often) where heads are 128 long
-// and a row sees some 6000 keys. 40 heads of 128, four waves against eight: 2048 x 2048
-// 93 and 108 us, 4096 x 4096 304 and 318, 8192 x 8192 1173 and 1127, 32760 x 32760 18.6
-// and 18.0 ms. 64 heads of 64, 16384 x 16384: 4.39 and 4.59 ms (the exponentials bound it).
-static int attention_waves(const mxq_attention_args& g) {
+// Keys that a row sees, about: a sequence's, or its window.
+static int64_t attention_keys(const mxq_attention_args& g) {
   const int64_t per = g.sequences > 0 ? g.Mk / g.sequences : 0;
-  const int64_t seen = g.left >= 0 && g.right >= 0 && g.left + g.right < per ? g.left + g.right : per;
-  return g.head_dim == 128 && seen >= 6144 ? 8 : 4;
+  return g.left >= 0 && g.right >= 0 && g.left + g.right < per ? g.left + g.right + 1 : per;
+}
+
+// Workgroups of four waves and 128 rows, two on a CU, which fill each other's waits; of
+// eight waves and 256 rows (a key tile is copied half as often) where heads are 128 long,
+// a row sees some 6000 keys and there are rows for all CUs. 40 heads of 128, four waves
+// against eight: 2048 x 2048 93 and 108 us, 4096 x 4096 304 and 318, 8192 x 8192 1173 and
+// 1127, 32760 x 32760 18.6 and 18.0 ms; 8 + 40 heads, 16 x 32000 30 and 41 us. 64 heads of 64,
+// 16384 x 16384: 4.39 and 4.59 ms (the exponentials bound it).
+static int attention_waves(const mxq_attention_args& g) {
+  return g.head_dim == 128 && attention_keys(g) >= 6144 && g.Mq * g.heads >= 256 * 256 ? 8 : 4;
 }
 
 static int64_t attention_slots(const mxq_attention_args& g) {
   return g.Mq * (g.heads / g.kv_heads) / (32 * attention_waves(g)) + g.sequences;
 }
 
-// Parts of the keys, so that few rows fill the chip, each of at least 8 tiles.
+// Parts of the keys, so that few rows fill the chip: a workgroup for each CU, or two where
+// one each would leave many CUs idle; two tiles a part at least; and no more than pays for
+// writing and joining the parts (some 1.2 us for each MB of a part, against 0.8 us a tile).
+// Keys in n parts, us: 16 x 8000, 40 + 8 heads of 128 n = 8, 16, 23 (taken), 48: 22.4, 17.1,
+// 16.6, 20.4; 37 x 30011, 64 + 8 heads of 64 n = 10, 21 (taken), 32: 39.8, 37.3, 39.7;
+// 100 x 4000, 40 + 40 of 128 n = 3, 6 (taken), 8, 16: 29.8, 25.5, 29.3, 36.4; 1000 x 1000,
+// 16 + 8 of 128 n = 1 (taken), 2, 4: 18.1, 22.5, 25.2.
 static int attention_splits(const mxq_attention_args& g) {
   const int64_t items = attention_slots(g) * g.kv_heads;
   if (items == 0) return 1;
-  int64_t s = 256 * (8 / attention_waves(g)) / items;
-  const int64_t tiles = (g.Mk + kKeys - 1) / kKeys;
-  if (s > tiles / 8) s = tiles / 8;
+  int64_t s = 256 / items;
+  if (512 / items > 2 * s) s = 512 / items;
+  const int64_t tiles = (attention_keys(g) + kKeys - 1) / kKeys;
+  if (s > tiles / 2) s = tiles / 2;
   if (s > 64) s = 64;
+  const int64_t part = g.Mq * g.heads * (g.head_dim + 2) * 4;
+  while (s > 1 && s * s * part > tiles * 1500000) --s;
   return s < 2 ? 1 : (int)s;
 }
 

@@ -15,7 +15,17 @@
 // go from memory straight into operand A of S^T = K Q^T (16x16x32 MFMAs, up to 16
 // query heads of a key head as columns); values pass through the wave's own LDS
 // for the transposing read that makes them operand A of O^T = V^T P^T, so the loop
-// has no barrier.
+// has no barrier. Scores, maxima, sums and O are fp32; the weights are rounded to bf16
+// for the second product (the sum takes them unrounded), out once. MXFP8 values are
+// exact in bf16 (4 bits of significand, the scale a power of two), so both formats
+// share the products; the scale is multiplied in on the way to them.
+//
+// One sequence of 131071, 40 + 8 heads of 128: 101 us, 5.3 TB/s (a copy: 4.9; a read
+// has no writes to turn the memory round for). 64 sequences, 262147 tokens in all, MXFP8:
+// 118 us, 4.7 TB/s. Both with the loads of a step issued before the arithmetic on the
+// step before: 102 and 124 us without. 9 sequences, window of 2048, heads of 64: 17.6 us
+// for 38 MB, 14 of them in this kernel: two steps a wave, so the chain of lengths,
+// table, keys, values and joins is what takes the time; then 3.5 us of join.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,7 +43,9 @@ typedef unsigned u32x4_v __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2_v __attribute__((ext_vector_type(2)));
 
 constexpr int kPagedThreads = 256, kPagedWaves = 4;
-constexpr int kMinUnits = 8;     // least run of a workgroup: 32 keys for each wave
+// Least run of a workgroup: 32 keys for each wave. Runs of 4, 8, 16 units at least, us, 40 + 8
+// heads of 128: 1 sequence of 500 9.5, 10.0, 11.8, 16 of 200 14.9, 13.5, 18.9.
+constexpr int kMinUnits = 8;
 constexpr int kPartRows = 16;    // query heads of a piece
 
 // Workgroups that share a CU: what the registers of the loads ahead leave (128-long heads
@@ -491,7 +503,8 @@ static hipError_t launch(const PagedArgs& a, bool fp8, hipStream_t s) {
     hipLaunchKernelGGL((paged_kernel<D, true>), dim3(a.workgroups), dim3(kPagedThreads), bytes, s, a);
   else
     hipLaunchKernelGGL((paged_kernel<D, false>), dim3(a.workgroups), dim3(kPagedThreads), bytes, s, a);
-  // few pieces to a sequence: a wave per head
+  // Few pieces to a sequence: a wave per head; many: a workgroup. The two against each other,
+  // us, 40 heads of 128: 1 sequence of 131071 107, 101; 16 of 8000 100, 100; 256 of 1000 188, 196.
   const int heads = a.sequences * a.kv_heads * a.group;
   if (a.sequences * a.kv_heads * a.qgroups * 4 > a.workgroups)
     hipLaunchKernelGGL((paged_join_kernel<D, 4>), dim3((heads + 3) / 4), dim3(kPagedThreads), 0, s, a);
