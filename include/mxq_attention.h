@@ -158,8 +158,8 @@ int mxq_rotary_qkv(const mxq_rotary_args* args, const mxq_kv_cache* cache, hipSt
  *   k, v       device bf16 [Mk][ldk], [Mk][ldv], kv_heads * head_dim elements a row
  *   starts_q, starts_k  device int32 [sequences + 1], not decreasing, or both null
  *              for one sequence of all rows
- *   scale      positive and finite
- * head_dim 64 or 128; heads a multiple of kv_heads; Mq, Mk below 2^29, and
+ *   scale      positive, below 2^127
+ * out may not overlap an input or the workspace. head_dim 64 or 128; heads a multiple of kv_heads; Mq, Mk below 2^29, and
  * Mq * heads / kv_heads below 2^31 - 256.
  * The workspace (mxq_attention_workspace_bytes; 0: it may be null) joins the parts
  * of a long axis when there are few rows. It belongs to the call until its work is
@@ -191,6 +191,8 @@ int mxq_attention(const mxq_attention_args* args, void* workspace, size_t worksp
  *   q, out       device bf16 [sequences][ldq], [sequences][ldo]
  *   block_table  device int32 [sequences][width]
  *   lengths      device int32 [sequences], at most 2^30
+ *   scale        positive, below 2^127
+ * out may not overlap an input, the cache or the workspace.
  * sequences * width * page_size below 2^34; heads a multiple of kv_heads.
  * The cache is split over workgroups by what the lengths say on the device; the
  * workspace (mxq_attention_paged_workspace_bytes) joins the parts.

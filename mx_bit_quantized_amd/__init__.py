@@ -676,7 +676,7 @@ def lowrank_up(y_pre, t, l2, epilogue=EPI_NONE, y=None, stream=None):
 _BLOCK = ("GATED_GELU_TANH", "GATED_SILU", "NORM_LAYER", "NORM_MAX_K", "NORM_NONE", "NORM_RMS", "block_kernel_name",
           "gemm_gated", "gemm_residual", "norm_quantize", "quantize_weight_gated_mxfp4")
 _ATTN = ("KV_BF16", "KV_MXFP8", "MAX_REQUESTS", "ROTARY_NORM_HEAD", "ROTARY_NORM_NONE", "ROTARY_NORM_ROW", "KvCache",
-              "PagePlan", "attention", "attention_paged", "kv_cache", "page_plan", "rotary_frequencies", "rotary_qkv")
+         "PagePlan", "attention", "attention_paged", "kv_cache", "page_plan", "rotary_frequencies", "rotary_qkv")
 
 
 def __getattr__(name):

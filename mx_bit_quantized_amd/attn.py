@@ -281,7 +281,7 @@ def _window(left, right, sinks):
             raise ValueError(f"{n} counts tokens, or -1 for no limit")
     if sinks < 0:
         raise ValueError("sinks must not be negative")
-    return left, right, sinks
+    return tuple(min(v, 1 << 62) for v in (left, right, sinks))
 
 
 def attention(q, k, v, starts_q=None, starts_k=None, scale=None, window=(-1, -1), sinks=0, out=None, stream=None):
@@ -291,7 +291,7 @@ def attention(q, k, v, starts_q=None, starts_k=None, scale=None, window=(-1, -1)
     starts_q, starts_k: int32 [sequences + 1], the rows where sequences start and the last one ends; without them all rows are
     one sequence. A sequence's queries are the last of its positions; with ``window = (left, right)`` the one at p sees keys
     p - left .. p + right (-1: no limit, right 0: causal) and the first ``sinks`` ones up to p + right. Rows that see nothing
-    are zeros, rows of ``out`` behind the last sequence stay. scale: 1 / sqrt(D) by default.
+    are zeros, rows of ``out`` behind the last sequence stay. scale: 1 / sqrt(D) by default. ``out`` may not overlap an input.
     """
     dev = _index(q, "q")
     if q.dim() != 3 or k.dim() != 3:
@@ -334,7 +334,8 @@ def attention_paged(q, cache, block_table, lengths, scale=None, window=-1, sinks
 
     q [sequences, heads, D], at position lengths[b] - 1 of sequence b, whose keys and values are the first lengths[b] tokens of
     the pages block_table[b] (int32 [sequences, width]); the new token's own k and v are in the cache already (rotary_qkv).
-    ``window`` is the number of earlier tokens that it sees (-1: all), besides the first ``sinks`` ones.
+    ``window`` is the number of earlier tokens that it sees (-1: all), besides the first ``sinks`` ones. ``out`` may not overlap an
+    input.
     """
     dev = _index(q, "q")
     if q.dim() != 3:

@@ -694,7 +694,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs a) {
 // Keys that a row sees, about: a sequence's, or its window.
 static int64_t attention_keys(const mxq_attention_args& g) {
   const int64_t per = g.sequences > 0 ? g.Mk / g.sequences : 0;
-  return g.left >= 0 && g.right >= 0 && g.left + g.right < per ? g.left + g.right + 1 : per;
+  return g.left >= 0 && g.right >= 0 && g.left < per && g.right < per - g.left ? g.left + g.right + 1 : per;
 }
 
 // Workgroups of four waves and 128 rows, two on a CU, which fill each other's waits; of

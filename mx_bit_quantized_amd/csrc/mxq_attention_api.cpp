@@ -54,6 +54,8 @@ int check_ld(int64_t ld, int64_t width) {
 }
 
 bool positive(float v) { return v > 0.0f && isfinite(v); }
+// (the kernels take scores in units of log2, scale / ln 2)
+bool score_scale(float v) { return positive(v) && v < 0x1p127f; }
 
 // MXQ_CHECK_FINITE on the rows of [rows][ld] that sequences own.
 int owned_guard(const char* what, const void* x, const int32_t* starts, int64_t sequences, int64_t rows, int64_t cols, int64_t ld,
@@ -76,7 +78,7 @@ int check_attention(const mxq_attention_args* args) {
   const mxq_attention_args& a = *args;
   int st = check_heads(a.heads, a.kv_heads);
   if (st != MXQ_OK) return st;
-  if (!positive(a.scale)) return MXQ_ERR_MODE;
+  if (!score_scale(a.scale)) return MXQ_ERR_MODE;
   if (!head_dim_ok(a.head_dim) || a.Mq < 0 || a.Mk < 0 || a.Mq >= kMaxRows / 2 || a.Mk >= kMaxRows / 2) return MXQ_ERR_SHAPE;
   if (a.sequences < 0 || a.sequences >= kMaxRows || a.sinks < 0) return MXQ_ERR_SHAPE;
   if ((a.starts_q == nullptr || a.starts_k == nullptr) && a.sequences != 1) return MXQ_ERR_SHAPE;
@@ -92,7 +94,7 @@ int check_paged(const mxq_paged_args* args, const mxq_kv_cache* cache) {
   const mxq_paged_args& a = *args;
   int st = check_cache_shape(*cache);
   if (st != MXQ_OK || (st = check_heads(a.heads, cache->kv_heads)) != MXQ_OK) return st;
-  if (!positive(a.scale)) return MXQ_ERR_MODE;
+  if (!score_scale(a.scale)) return MXQ_ERR_MODE;
   if (a.sequences < 0 || a.sequences > MXQ_MAX_REQUESTS || a.width <= 0 || a.width >= kMaxRows || a.sinks < 0) return MXQ_ERR_SHAPE;
   if (a.sequences * a.width >= (int64_t(1) << 34) / cache->page_size) return MXQ_ERR_SHAPE;
   const int64_t wq = (int64_t)a.heads * cache->head_dim;
