@@ -315,7 +315,7 @@ ATTENTION = [  # lens, heads, kv, d, left, right, sinks
     ([(17, 64 * 40 + 5)], 16, 1, 64, -1, 0, 0),    # few rows, a long axis: joined from parts
     ([(5, 4096)], 3, 3, 128, -1, -1, 0),
     ([(5, 4096)], 3, 3, 128, 1000, 0, 70),
-    ([(300, 6300)], 2, 1, 128, -1, 0, 0),          # long axes of heads of 128: workgroups of 256 rows
+    ([(300, 6300)], 2, 1, 128, -1, 0, 0),          # long axes of heads of 128
     ([(513, 6145)], 1, 1, 128, -1, -1, 0),
     ([(70, 7000), (200, 6500), (0, 20), (3, 13000)], 3, 1, 128, -1, 5, 0),
     ([(130, 12700)], 4, 2, 128, 6100, 200, 3),
