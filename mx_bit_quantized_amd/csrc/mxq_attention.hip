@@ -672,7 +672,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs a) {
     o.w = o.w * f + v.w * w;
   };
   if (live)
-#pragma unroll 4
+#pragma unroll 8  // loads under way together: 21 parts of 2368 rows 5.2 us, by four 5.5
     for (int s = which; s < a.splits; s += kJoin) {
       const float2 p = *reinterpret_cast<const float2*>(ml + 2 * (s * total + r));
       add(p.x, p.y, *reinterpret_cast<const float4*>(a.part + (s * total + r) * D + c));

@@ -466,7 +466,7 @@ __global__ __launch_bounds__(kPagedThreads) void paged_join_kernel(const PagedAr
     v.w = v.w * f + x.w * w;
   };
   if (i0 < i1)
-#pragma unroll 2
+#pragma unroll 4  // loads under way together: 64 pieces a head 4.9 us, by two 5.5, by eight 8.7
     for (int64_t i = i0 + which; i <= i1; i += AHEAD) {
       const int64_t at = (2 * i + (i == i0 ? 1 : 0)) * kPartRows + row;
       const float2 p = *reinterpret_cast<const float2*>(ml + 2 * at);
