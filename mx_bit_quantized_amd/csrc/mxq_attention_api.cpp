@@ -135,11 +135,11 @@ int mxq_rotary_qkv(const mxq_rotary_args* args, const mxq_kv_cache* cache, hipSt
   if (a.norm != MXQ_ROTARY_NORM_NONE && !positive(a.eps)) return MXQ_ERR_MODE;
   if (a.norm == MXQ_ROTARY_NORM_NONE && (a.q_weight != nullptr || a.k_weight != nullptr)) return MXQ_ERR_MODE;
   if (a.interleaved != 0 && a.interleaved != 1) return MXQ_ERR_MODE;
-  if (!head_dim_ok(a.head_dim) || a.heads < 0 || a.kv_heads < 0 || a.heads + a.kv_heads == 0) return MXQ_ERR_SHAPE;
-  if (a.heads > kMaxHeads || a.kv_heads > kMaxHeads) return MXQ_ERR_SHAPE;
+  if (!head_dim_ok(a.head_dim) || a.heads < 0 || a.kv_heads < 0 || a.heads > kMaxHeads || a.kv_heads > kMaxHeads) return MXQ_ERR_SHAPE;
+  if (a.heads == 0 && a.kv_heads == 0) return MXQ_ERR_SHAPE;
   const int64_t width = (a.heads + 2 * (int64_t)a.kv_heads) * a.head_dim;
   if (width > 65536 || a.M < 0 || a.M >= kMaxRows || (st = check_ld(a.ldx, width)) != MXQ_OK) return MXQ_ERR_SHAPE;
-  if (a.pairs < 0 || a.pairs % 8 != 0 || 2 * a.pairs > a.head_dim) return MXQ_ERR_SHAPE;
+  if (a.pairs < 0 || a.pairs % 8 != 0 || a.pairs > a.head_dim / 2) return MXQ_ERR_SHAPE;
   if (a.pairs > 0 && (a.axes < 1 || a.ld_pos < a.M || a.ld_pos >= kMaxDim)) return MXQ_ERR_SHAPE;
   if (a.q != nullptr && (st = check_ld(a.ldq, (int64_t)a.heads * a.head_dim)) != MXQ_OK) return st;
   if (a.k != nullptr && (st = check_ld(a.ldk, (int64_t)a.kv_heads * a.head_dim)) != MXQ_OK) return st;
