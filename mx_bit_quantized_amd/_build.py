@@ -105,15 +105,28 @@ def build(verbose=True):
     return LIB
 
 
+_sanitized = {}  # newest change of the sources -> where this process has built them sanitized
+
+
 def build_host_sanitized(out_path, verbose=False):
     """The library's host code under AddressSanitizer + UndefinedBehaviorSanitizer, for host-side tests.
 
     The sanitizers instrument the host side only (each -fsanitize= behind
     -Xarch_host); the device code is the ordinary gfx950 build. Load it with
-    the clang ASan runtime preloaded (sanitizer_runtime())."""
+    the clang ASan runtime preloaded (sanitizer_runtime()). The build takes
+    minutes, so a process makes it once: a second call copies the first one's
+    library if no source has changed since."""
+    import shutil
+
+    newest = max(os.stat(os.path.join(d, f)).st_mtime_ns for d in (CSRC, INCLUDE) for f in os.listdir(d))
+    before = _sanitized.get(newest)
+    if before is not None and os.path.exists(before):
+        shutil.copyfile(before, out_path)
+        return out_path
     flags = DEVICE_FLAGS + COMMON_FLAGS + ["-g", "-fno-omit-frame-pointer", "-Xarch_host", "-fsanitize=address",
                                            "-Xarch_host", "-fsanitize=undefined", "-shared-libsan"]
     _compile_and_link(flags, [os.path.join(CSRC, s) for s in DEVICE_SOURCES], out_path, verbose)
+    _sanitized[newest] = out_path
     return out_path
 
 
