@@ -104,7 +104,9 @@ int mxq_page_plan(const int32_t* cached, const int32_t* added, int32_t* block_ta
  *   pair p of a head, (a, b) = (n[2p], n[2p + 1]) interleaved, (n[p], n[p + pairs])
  *   else, turned by the angle t = positions[axis[p]][m] * freqs[p]:
  *   (a cos t - b sin t, a sin t + b cos t)
- * and one rounding to bf16. The elements behind the 2 * pairs turned ones, and
+ * and one rounding to bf16. Values whose squares sum past fp32's range (|x| about
+ * 1e18) are not finite inputs of a norm: the row's q or k, or the head, is NaN,
+ * which MXQ_CHECK_FINITE reports. The elements behind the 2 * pairs turned ones, and
  * pairs whose axis is not in 0 .. axes - 1, are only normed. The angle is formed
  * and reduced in 64 bits. v is only copied into the cache.
  *   qkv        device bf16 [M][ldx]

@@ -89,6 +89,13 @@ __device__ __forceinline__ uint32_t mxfp8_scale_byte(uint32_t amax_bits) {
   return b < 0 ? 0u : (uint32_t)b;
 }
 
+// 1 / sqrt(mean square + eps). A sum of squares past fp32's range is no norm: 0 times its
+// infinity makes the row NaN, where 1 / sqrt(infinity) = 0 would leave zeros.
+__device__ __forceinline__ float inverse_norm(float sum, float inv_n, float eps) {
+  const float v = sum * inv_n + eps;
+  return __builtin_fmaf(v, 0.0f, __builtin_amdgcn_rsqf(v));
+}
+
 // Rotations of 8 elements by the pairs' cosines and sines: four pairs side by side,
 // or eight pairs of one chunk with the other.
 __device__ __forceinline__ void turn_interleaved(float (&f)[8], const float* cs, const float* sn) {
@@ -249,8 +256,8 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
           sq += red[buf][r][0][w];
           sk += red[buf][r][1][w];
         }
-        iq = __builtin_amdgcn_rsqf(sq * a.inv_q + a.eps);
-        ik = __builtin_amdgcn_rsqf(sk * a.inv_k + a.eps);
+        iq = inverse_norm(sq, a.inv_q, a.eps);
+        ik = inverse_norm(sk, a.inv_k, a.eps);
       }
       int64_t slot = -1;
       if (a.ck != nullptr) {
@@ -267,7 +274,7 @@ __global__ __launch_bounds__(1024) void rotary_qkv_kernel(const RotaryArgs a) {
           float s = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) s += f[e] * f[e] + g[e] * g[e];
-          inv = __builtin_amdgcn_rsqf(head_sum(s, wide) * (wide ? 1.0f / 128.0f : 1.0f / 64.0f) + a.eps);
+          inv = inverse_norm(head_sum(s, wide), wide ? 1.0f / 128.0f : 1.0f / 64.0f, a.eps);
         }
         uint4 y0 = x0[u][r], y1 = x1[u][r];
         if (part[u] < 2) {

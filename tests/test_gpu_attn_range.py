@@ -1,0 +1,68 @@
+"""GPU tests of the attention half at the ends of what its inputs may hold: very large and very small numbers, and where the
+arithmetic leaves fp32's range. Tolerances: those of test_gpu_attn.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import mx_bit_quantized_amd as mxq
+import oracle
+from test_gpu_attn import BF16, DEV, attention_check, gen, host, ints, randn, rotary_want, rotary_within, say, within
+from test_gpu_check_finite import guard
+
+pytestmark = pytest.mark.gpu
+
+
+def reported(call):
+    with guard(True), pytest.raises(mxq.MxqError) as e:
+        call()
+    assert e.value.status == mxq.ERR_NONFINITE
+
+
+# ------------------------------------------------------- norms of rotary_qkv ----
+
+NORMED = [(3, 4, 2, 64), (4, 128, 128, 128), (3, 170, 170, 128), (2051, 40, 8, 128)]  # one, two, four units a thread; two rows a step
+
+
+def normed_case(m, heads, kv, d, norm, value):
+    g = gen(heads + m)
+    x = randn(g, m, (heads + 2 * kv) * d, scale=2.0)
+    of = (heads * d, kv * d) if norm == 1 else (d, d)
+    weights = [(1 + 0.2 * torch.randn(n, generator=g)).to(BF16) for n in of]
+    if value is not None:
+        x[1, 3 * d + 9] = value                    # q, head 3
+        x[m - 1, (heads + kv - 1) * d + 40] = -value  # k, its last head
+    call = lambda **more: mxq.rotary_qkv(x.to(DEV), heads, kv, d, norm=norm, q_weight=weights[0].to(DEV), k_weight=weights[1].to(DEV),
+                                         **more)
+    return x, weights, call
+
+
+@pytest.mark.parametrize("norm", [mxq.ROTARY_NORM_ROW, mxq.ROTARY_NORM_HEAD])
+@pytest.mark.parametrize("m, heads, kv, d", NORMED)
+def test_rotary_norms_past_the_range(m, heads, kv, d, norm):
+    """The row (or head) is NaN, dense and in the cache, everything else stays; the guard reports it."""
+    say("norm range", m, heads, kv, d, norm)
+    held = mxq.kv_cache(m // 16 + 1, kv, 16, d)
+    want_q, want_k = normed_case(m, heads, kv, d, norm, None)[2]()
+    call = normed_case(m, heads, kv, d, norm, 2e19)[2]
+    q, k = call(cache=held, slots=ints(list(range(m))))
+    bad_q, bad_k = torch.zeros(m, heads, dtype=torch.bool, device=DEV), torch.zeros(m, kv, dtype=torch.bool, device=DEV)
+    bad_q[1, slice(None) if norm == mxq.ROTARY_NORM_ROW else 3] = True
+    bad_k[m - 1, slice(None) if norm == mxq.ROTARY_NORM_ROW else kv - 1] = True
+    kept = held.k.transpose(1, 2).reshape(-1, kv, d)[:m]
+    for got, bad, want in ((q, bad_q, want_q), (k, bad_k, want_k), (kept, bad_k, want_k)):
+        assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+    reported(call)
+
+
+@pytest.mark.parametrize("norm", [mxq.ROTARY_NORM_ROW, mxq.ROTARY_NORM_HEAD])
+@pytest.mark.parametrize("m, heads, kv, d", NORMED)
+def test_rotary_norms_inside_the_range(m, heads, kv, d, norm):
+    """2^63, whose square is 2^126, among ordinary numbers."""
+    say("norm inside", m, heads, kv, d, norm)
+    x, weights, call = normed_case(m, heads, kv, d, norm, 2.0 ** 63)
+    some = sorted({0, 1, m - 1})
+    want = rotary_want(x[some], heads, kv, d, torch.zeros(0, dtype=torch.float64), [], None, weights, norm, False)
+    q, k = call()
+    rotary_within(q[some], want[0], "q")
+    rotary_within(k[some], want[1], "k")
