@@ -780,7 +780,9 @@ hipError_t launch_attention(const mxq_attention_args& g, void* workspace, hipStr
   // row. Factors 2^0, 2^3, 2^8: 32760 x 32760 18.0, 17.5, 17.3 ms with a relative error of
   // .0022, .0024, .0025; 65520 queries of two sequences against 741 keys 700, 693, 678 us
   // with .0019, .0022, .0025.
-  a.slack = 3.0f / a.scale_log2;
+  // (finite, for scales near 0: -infinity of a row that has seen nothing and an infinite slack
+  // would be NaN, which no score exceeds)
+  a.slack = fminf(3.0f / a.scale_log2, 3.4e38f);
   if (g.head_dim == 64) return launch<64, 4>(a, s);
   return attention_waves(g) == 8 ? launch<128, 8>(a, s) : launch<128, 4>(a, s);
 }

@@ -66,3 +66,25 @@ def test_rotary_norms_inside_the_range(m, heads, kv, d, norm):
     q, k = call()
     rotary_within(q[some], want[0], "q")
     rotary_within(k[some], want[1], "k")
+
+
+# -------------------------------------------------------- scales of attention ----
+
+@pytest.mark.parametrize("d, group", [(64, 1), (128, 4)])
+@pytest.mark.parametrize("scale", [1e-38, 1e-39, 1e-45, 1e-30])
+def test_attention_scales_near_zero(scale, d, group):
+    """Rows that see nothing of a part's first tile, other rows of their wave do, and a scale whose inverse overflows."""
+    nq, nk, left = 40, 20000, 2946
+    say("scale", scale, d, group)
+    g = gen(d)
+    q, k = randn(g, nq, group, d), randn(g, nk, 1, d)
+    v = torch.zeros(nk, 1, d, dtype=BF16)
+    v[17024:17088] = 8.0  # (in the first part of the keys; the rows' windows begin at 17014 to 17053)
+    out = mxq.attention(q.to(DEV), k.to(DEV), v.to(DEV), window=(left, 0), scale=scale)
+    attention_check(out, q, k, v, [(nq, nk)], left, 0, 0, scale, "scale")
+    # ragged sequences of few keys, in one part
+    lens = [(50, 200), (3, 1), (70, 70)]
+    q, k, v = (randn(g, 123, group, d), randn(g, 271, 1, d), randn(g, 271, 1, d))
+    starts = [ints(np.concatenate([[0], np.cumsum([n[i] for n in lens])]).tolist()) for i in range(2)]
+    out = mxq.attention(q.to(DEV), k.to(DEV), v.to(DEV), *starts, window=(30, 0), sinks=2, scale=scale)
+    attention_check(out, q, k, v, lens, 30, 0, 2, scale, "scale, ragged")
