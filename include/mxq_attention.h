@@ -154,7 +154,10 @@ int mxq_rotary_qkv(const mxq_rotary_args* args, const mxq_kv_cache* cache, hipSt
  * over the visible keys, in fp32 from fp32 scores; the w_j enter the product with
  * v as bf16 values (relative to the largest one of the keys seen so far), and out
  * is rounded to bf16 once. A row without visible keys is zeros, and so is one whose
- * scores are all -infinity. Keys and values at places that a query does not see may
+ * scores are all -infinity. A row whose largest score (scale q . k) is past 7e8 in
+ * magnitude, where fp32 holds no exponents any more, is NaN, and sums of weighted
+ * values past fp32's range are infinities: MXQ_CHECK_FINITE reports both. Keys and
+ * values at places that a query does not see may
  * hold anything. Rows of out behind the last sequence are left as they were.
  *   q, out     device bf16 [Mq][ldq], [Mq][ldo], heads * head_dim elements a row
  *   k, v       device bf16 [Mk][ldk], [Mk][ldv], kv_heads * head_dim elements a row

@@ -402,7 +402,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : 2) void attention_kernel(con
     const float alpha = now == m ? 1.0f : __builtin_amdgcn_exp2f((m - now) * a.scale_log2);
     m = now;
     bar = now + a.slack;
-    shift = now == -__builtin_inff() ? 0.0f : -now * a.scale_log2;
+    shift = score_shift(now, a.scale_log2);
     sum[0] *= alpha;
     sum[1] *= alpha;
 #pragma unroll
@@ -615,13 +615,13 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : 2) void attention_kernel(con
         *reinterpret_cast<float4*>(dst + 32 * d + 2 * r + 4 * half) = make_float4(o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]);
     if (half == 0) {
       float* ml = a.part + (int64_t)a.splits * a.Mq * (a.kv_heads * a.group) * D + 2 * at;
-      ml[0] = m * a.scale_log2;
+      ml[0] = row_top(m, a.scale_log2);
       ml[1] = l;
     }
   } else {
     // through LDS, so that rows leave whole: 8 bytes a lane in, 16 bytes a lane out, chunks
     // permuted like those of K
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = row_inverse(row_top(m, a.scale_log2), l);
     const uint32_t mine = lds0 + (NW == 4 ? 2 * TILE : 0) + wave * 64 * D;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -686,7 +686,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs a) {
   if (which != 0 || !live) return;
 #pragma unroll
   for (int s = 1; s < kJoin; ++s) add(sml[local][s][0], sml[local][s][1], *reinterpret_cast<const float4*>(&so[local][s][c]));
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = row_inverse(top, l);
   *reinterpret_cast<uint2*>(a.out + row * a.ldo + (r - row * heads) * D + c) =
       make_uint2(bf16x2_rne(o.x * inv, o.y * inv), bf16x2_rne(o.z * inv, o.w * inv));
 }

@@ -195,4 +195,26 @@ __device__ __forceinline__ void fwht128_lanes(float (&f)[8], int c) {
 #undef MXQ_DPP_FMAC
 }
 
+// Softmax statistics of the attention kernels. A weight is 2^(s c + shift) in one fma, with
+// shift = -round(m c) for a running maximum m: the rounding is common to a row's weights and
+// leaves their ratios, but moves them all by up to half a step of m c. Below 2^30 that is a
+// factor 2^32, inside fp32's range; past it all weights may become zeros or infinities. There
+// they are zeros (a later score inside the range takes over), and a row that ends there is
+// NaN, not the zeros of a row that sees nothing.
+constexpr float kMaxScore = 0x1p30f;  // in units of log2
+
+__device__ __forceinline__ float score_shift(float m, float scale_log2) {
+  const float t = m * scale_log2;
+  return __builtin_fabsf(t) < kMaxScore ? -t : -__builtin_inff();  // (m = -infinity: nothing seen, all weights 0)
+}
+// A row's largest score in units of log2, -infinity only if that is what it is.
+__device__ __forceinline__ float row_top(float m, float scale_log2) {
+  return m == -__builtin_inff() ? m : fmaxf(m * scale_log2, -3.4e38f);
+}
+// 1 / the sum of a row's weights.
+__device__ __forceinline__ float row_inverse(float top, float sum) {
+  if (top > -__builtin_inff() && !(__builtin_fabsf(top) < kMaxScore)) return __builtin_nanf("");
+  return sum == 0.0f ? 0.0f : 1.0f / sum;
+}
+
 }  // namespace mxq

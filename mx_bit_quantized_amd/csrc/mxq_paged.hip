@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kPagedThreads, workgroups_per_cu(D)) void paged_ker
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) o[d] *= alpha;
       }
-      const float shift = m == -__builtin_inff() ? 0.0f : -m * a.scale_log2;
+      const float shift = score_shift(m, a.scale_log2);
       float e[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(kPagedThreads, workgroups_per_cu(D)) void paged_ker
     l = quarter_sum(l);
     __syncthreads();
     if (g4 == 0) {
-      join_ml[wave][n16][0] = m * a.scale_log2;
+      join_ml[wave][n16][0] = row_top(m, a.scale_log2);
       join_ml[wave][n16][1] = l;
     }
     float* const jo = reinterpret_cast<float*>(lds) + wave * 16 * D;
@@ -403,7 +403,7 @@ __global__ __launch_bounds__(kPagedThreads, workgroups_per_cu(D)) void paged_ker
         v.w += f * x.w;
       }
       if (whole) {
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = row_inverse(top, sum);
         *reinterpret_cast<uint2*>(a.out + (int64_t)b * a.ldo + (int64_t)(head0 + row) * D + c) =
             make_uint2(bf16x2_rne(v.x * inv, v.y * inv), bf16x2_rne(v.z * inv, v.w * inv));
       } else {
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(kPagedThreads) void paged_join_kernel(const PagedAr
     for (int i = 1; i < AHEAD; ++i) add(sml[mine][i][0], sml[mine][i][1], *reinterpret_cast<const float4*>(&so[mine][i][4 * lane]));
   }
   if (units > 0 && i0 == i1) return;  // written by the first kernel
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = row_inverse(top, sum);
   *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_rne(v.x * inv, v.y * inv), bf16x2_rne(v.z * inv, v.w * inv));
 }
 

@@ -88,3 +88,80 @@ def test_attention_scales_near_zero(scale, d, group):
     starts = [ints(np.concatenate([[0], np.cumsum([n[i] for n in lens])]).tolist()) for i in range(2)]
     out = mxq.attention(q.to(DEV), k.to(DEV), v.to(DEV), *starts, window=(30, 0), sinks=2, scale=scale)
     attention_check(out, q, k, v, lens, 30, 0, 2, scale, "scale, ragged")
+
+
+SCORED = [(3, 50, (-1, -1)), (70, 70, (-1, 0)), (2, 8000, (-1, -1)), (40, 300, (20, 0)), (1030, 6200, (-1, -1))]
+
+
+def first_elements(q0, k0, nq, nk, heads, d, seed):
+    """Queries and keys whose first elements alone make scores, and values: bf16."""
+    q, k = torch.zeros(nq, heads, d), torch.zeros(nk, 1, d)
+    q[..., 0], k[..., 0] = q0, k0
+    return q.to(BF16), k.to(BF16), randn(gen(seed), nk, 1, d)
+
+
+def paged_of(k, v, page=16):
+    """The rows as the pages of one sequence: (cache, table)."""
+    pages = -(-len(k) // page)
+    held = []
+    for t in (k, v):
+        rows = torch.zeros(pages * page, *t.shape[1:], dtype=BF16)
+        rows[:len(t)] = t
+        held.append(rows.view(pages, page, *t.shape[1:]).transpose(1, 2).contiguous().to(DEV))
+    return mxq.KvCache(*held), ints([list(range(pages))])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq, nk, window", SCORED)
+def test_attention_scores_past_the_range(nq, nk, window, d):
+    """Largest scores past 2^30 (in units of log2), finite ones and ones whose product with the scale is not: NaN, not the zeros of a
+    row that sees nothing. Below it, rows of equal scores are means of values."""
+    say("scores", nq, nk, window, d)
+    heads = 64 if nq > 1000 else 2
+    for q0, k0, scale, fine in ((2.0 ** 60, 2.0 ** 60, 1024.0, False), (2.0 ** 60, 2.0 ** 60, 1.0, False), (1.3e6, 1.1e6, 0.125, False),
+                                (-(2.0 ** 60), 2.0 ** 60, 1.0, False), (-(2.0 ** 60), 2.0 ** 60, 1024.0, False),
+                                (-1.3e6, 1.1e6, 0.125, False), (70000.0, 70000.0, 0.125, True), (-70000.0, 70000.0, 0.125, True)):
+        q, k, v = first_elements(q0, k0, nq, nk, heads, d, nk)
+        a = [t.to(DEV) for t in (q, k, v)]
+        call = lambda: mxq.attention(*a, window=window, scale=scale)
+        if fine:
+            # (equal scores: the rounding of the exponent's argument is common to all weights and cancels)
+            attention_check(call(), torch.zeros_like(q), k, v, [(nq, nk)], *window, 0, 1.0, "equal scores", heads=[0, heads - 1])
+        else:
+            assert torch.isnan(call()).all(), (q0, k0, scale)
+            reported(call)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [3, 40, 5000])
+def test_attention_paged_scores_past_the_range(n, d):
+    say("scores, paged", n, d)
+    for q0, k0, scale, fine in ((2.0 ** 60, 2.0 ** 60, 1024.0, False), (2.0 ** 60, 2.0 ** 60, 1.0, False), (1.3e6, 1.1e6, 0.125, False),
+                                (-(2.0 ** 60), 2.0 ** 60, 1024.0, False), (-1.3e6, 1.1e6, 0.125, False),
+                                (70000.0, 70000.0, 0.125, True), (-70000.0, 70000.0, 0.125, True)):
+        q, k, v = first_elements(q0, k0, 1, n, 2, d, n)
+        held, table = paged_of(k, v)
+        call = lambda: mxq.attention_paged(q.to(DEV), held, table, ints([n]), scale=scale)
+        if fine:
+            attention_check(call(), torch.zeros_like(q), k, v, [(1, n)], -1, -1, 0, 1.0, "equal scores")
+        else:
+            assert torch.isnan(call()).all(), (q0, k0, scale)
+            reported(call)
+
+
+@pytest.mark.parametrize("nk, begin, end", [(300, 0, 70), (300, 130, 300), (9000, 0, 4100), (9000, 4000, 9000), (9000, 1, 9000)])
+def test_attention_scores_far_below_the_others(nk, begin, end):
+    """Keys whose scores are past the range below have no weight next to ordinary ones, wherever they lie."""
+    say("far below", nk, begin, end)
+    d, heads = 128, 2
+    g = gen(nk + begin)
+    q, k, v = randn(g, 3, heads, d), randn(g, nk, 1, d), randn(g, nk, 1, d)
+    q[..., 0], k[..., 0] = 3e5, 0.0
+    k[begin:end, :, 0] = -3e12
+    keep = torch.tensor([j for j in range(nk) if not begin <= j < end])
+    for window in ((-1, -1), (nk, 2)):
+        out = mxq.attention(q.to(DEV), k.to(DEV), v.to(DEV), window=window)
+        attention_check(out, q, k[keep], v[keep], [(3, len(keep))], -1, -1, 0, d ** -0.5, "below")
+    held, table = paged_of(k, v)
+    out = mxq.attention_paged(q[:1].to(DEV), held, table, ints([nk]))
+    attention_check(out, q[:1], k[keep], v[keep], [(1, len(keep))], -1, -1, 0, d ** -0.5, "below, paged")
