@@ -44,7 +44,9 @@ extern "C" {
 
 /* Formats of a key-value cache. MXQ_KV_MXFP8: OCP MX blocks of 32 elements along
  * a head, E4M3 elements and one E8M0 scale 2^(floor(log2 amax) - 8), rounded to
- * nearest even and saturating at 448 (as the MXFP4 of mxq.h with wider elements). */
+ * nearest even and saturating at 448 (as the MXFP4 of mxq.h with wider elements).
+ * A NaN stays one (code 0x7F or 0xFF) and an infinity reads as one, but the finite
+ * values of their block are lost to its scale. */
 enum { MXQ_KV_BF16 = 0, MXQ_KV_MXFP8 = 1 };
 
 /* RMS norms of q and k: none, over all heads of a row, or per head. */

@@ -68,13 +68,15 @@ __device__ __forceinline__ uint32_t head_max(uint32_t v, bool wide) {
   return wide ? umax(v, o) : v;
 }
 
-// 8 bf16 -> 8 E4M3 codes of a block with scale 2^(sb - 127), saturating at 448.
+// 8 bf16 -> 8 E4M3 codes of a block with scale 2^(sb - 127), saturating at 448. (A NaN is kept:
+// the median of it and the two bounds would be a bound, and a key of -infinity drops out of
+// attention without a trace.)
 __device__ __forceinline__ uint2 pack8_mxfp8(const uint4 c, uint32_t sb) {
   float f[8];
   bf16x8_to_f32(c, f);
   const float inv = as_float((254u - sb) << 23);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __builtin_amdgcn_fmed3f(f[i] * inv, -448.0f, 448.0f);
+  for (int i = 0; i < 8; ++i) f[i] = f[i] != f[i] ? f[i] : __builtin_amdgcn_fmed3f(f[i] * inv, -448.0f, 448.0f);
   uint2 o;
   o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
   o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], (int)o.x, true);

@@ -165,3 +165,69 @@ def test_attention_scores_far_below_the_others(nk, begin, end):
     held, table = paged_of(k, v)
     out = mxq.attention_paged(q[:1].to(DEV), held, table, ints([nk]))
     attention_check(out, q[:1], k[keep], v[keep], [(1, len(keep))], -1, -1, 0, d ** -0.5, "below, paged")
+
+
+# ------------------------------------------------- numbers into an MXFP8 cache ----
+
+@pytest.mark.parametrize("d, kv", [(64, 1), (128, 3)])
+def test_mxfp8_cache_of_large_and_small_numbers(d, kv):
+    """Blocks of every magnitude that bf16 has, the largest and subnormal ones among them: codes and scales as defined, and what
+    attention reads of a single token is its value."""
+    say("magnitudes", d, kv)
+    g, m, page = gen(d), 262, 16
+    v = torch.randn(m, 2 * kv, d, generator=g) * torch.exp2(torch.arange(m) - 134.0)[:, None, None].double()
+    x = v.clamp(-3.3895e38, 3.3895e38).to(BF16)
+    x[m - 1, :, 3], x[m - 2, :, 40] = 3.3895e38, -3.3895e38
+    assert torch.isfinite(x).all()
+    held = mxq.kv_cache(-(-m // page), kv, page, d, mxq.KV_MXFP8)
+    for t in held:
+        t.fill_(0x55)
+    _, dense = mxq.rotary_qkv(x.view(m, -1).to(DEV), 0, kv, d, cache=held, slots=ints(list(range(m))))
+    assert torch.equal(dense.cpu(), x[:, :kv])
+    rows = []
+    for codes, scales, value in ((held.k, held.k_scales, x[:, :kv]), (held.v, held.v_scales, x[:, kv:])):
+        c, s = oracle.mxfp8_quantize(host(value))
+        got = [t.cpu().transpose(1, 2).reshape(-1, kv, t.shape[3])[:m] for t in (codes, scales)]
+        bits = np.where(c & 0x7F, 0xFF, 0x7F).astype(np.uint8)  # (a zero may have either sign)
+        assert np.array_equal(got[0].numpy() & bits, c & bits)
+        assert torch.equal(got[1], torch.from_numpy(s))
+        rows.append(oracle.mxfp8_dequantize(c, s))
+    # tokens at the start of their page, one to a sequence: the output is the value that the cache stands for, where bf16 has it
+    # to all its bits (2^-126 on)
+    first = list(range(0, m, page))
+    q = torch.zeros(len(first), kv, d, dtype=BF16, device=DEV)
+    out = host(mxq.attention_paged(q, held, ints([[i] for i in range(len(first))]), ints([1] * len(first))))
+    want = rows[1][first]
+    assert np.array_equal(np.where(np.abs(want) < 2.0 ** -126, 0, out), np.where(np.abs(want) < 2.0 ** -126, 0, want))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_caches_keep_infinities_and_nan(d):
+    """What is not finite among keys and values shows in the same places of the output, whichever format the cache has."""
+    say("not finite", d)
+    kv, heads, m, nan, inf = 2, 4, 40, float("nan"), float("inf")
+    base = randn(gen(d), m, (heads + 2 * kv) * d)
+    base[:, :heads * d] = base[:, :heads * d].abs() + 0.1  # (an infinite key has a score of its sign)
+    key, value = heads * d, (heads + kv) * d
+    for name, places in (("nan key", [(7, key + 5, nan)]), ("-nan key", [(39, key + d + 33, -nan)]), ("nan value", [(7, value + 9, nan)]),
+                         ("nan values", [(0, value, nan), (17, value + 2 * d - 1, nan)]), ("inf key", [(20, key + 1, inf)]),
+                         ("inf values", [(3, value + 31, inf), (4, value + d + 32, -inf)])):
+        x = base.clone()
+        for r, c, what in places:
+            x[r, c] = what
+        seen = []
+        for fmt in (mxq.KV_BF16, mxq.KV_MXFP8):
+            held = mxq.kv_cache(3, kv, 16, d, fmt)
+            q, _ = mxq.rotary_qkv(x.to(DEV), heads, kv, d, cache=held, slots=ints(list(range(m))), write_k=False)
+            out = mxq.attention_paged(q[-1:], held, ints([[0, 1, 2]]), ints([m])).float().cpu()
+            seen.append((torch.isnan(out), torch.isposinf(out), torch.isneginf(out)))
+        for a, b in zip(*seen):
+            assert torch.equal(a, b), name
+        assert any(a.any() for a in seen[0]), name
+        group = heads // kv  # only the heads that read the place
+        for r, c, what in places:
+            hk = (c - (key if c < value else value)) // d
+            hit = torch.stack(seen[0]).any(0)[0]
+            assert hit[hk * group:(hk + 1) * group].any(), name
+        if "key" in name:
+            assert hit[hk * group:(hk + 1) * group].all() and not hit[(1 - hk) * group:(2 - hk) * group].any(), name
