@@ -132,7 +132,8 @@ int mxq_rotary_qkv(const mxq_rotary_args* args, const mxq_kv_cache* cache, hipSt
   const mxq_rotary_args& a = *args;
   int st;
   if (a.norm != MXQ_ROTARY_NORM_NONE && a.norm != MXQ_ROTARY_NORM_ROW && a.norm != MXQ_ROTARY_NORM_HEAD) return MXQ_ERR_MODE;
-  if (a.norm != MXQ_ROTARY_NORM_NONE && !positive(a.eps)) return MXQ_ERR_MODE;
+  // (the kernel's reciprocal square root takes normal numbers)
+  if (a.norm != MXQ_ROTARY_NORM_NONE && !(a.eps >= 0x1p-126f && isfinite(a.eps))) return MXQ_ERR_MODE;
   if (a.norm == MXQ_ROTARY_NORM_NONE && (a.q_weight != nullptr || a.k_weight != nullptr)) return MXQ_ERR_MODE;
   if (a.interleaved != 0 && a.interleaved != 1) return MXQ_ERR_MODE;
   if (!head_dim_ok(a.head_dim) || a.heads < 0 || a.kv_heads < 0 || a.heads > kMaxHeads || a.kv_heads > kMaxHeads) return MXQ_ERR_SHAPE;

@@ -47,3 +47,11 @@ def test_paged_refuses_counts(change):
 @pytest.mark.parametrize("change", [{n: v} for n in ("page", "requests", "width", "n_free", "tokens") for v in (I64_MAX, I64_MIN)])
 def test_page_plan_refuses_counts(change):
     assert plan(**change) == mxq.ERR_SHAPE
+
+
+@pytest.mark.parametrize("norm", [mxq.ROTARY_NORM_ROW, mxq.ROTARY_NORM_HEAD])
+@pytest.mark.parametrize("eps", [1e-40, 2.0 ** -127, 2.0 ** -149, -1e-6])
+def test_rotary_refuses_subnormal_eps(eps, norm):
+    assert rotary(eps=eps, norm=norm) == mxq.ERR_MODE
+    assert rotary(eps=2.0 ** -126, norm=norm, M=0) == mxq.OK
+    assert rotary(eps=eps, norm=mxq.ROTARY_NORM_NONE, q_weight=None, k_weight=None, M=0) == mxq.OK

@@ -231,3 +231,23 @@ def test_caches_keep_infinities_and_nan(d):
             assert hit[hk * group:(hk + 1) * group].any(), name
         if "key" in name:
             assert hit[hk * group:(hk + 1) * group].all() and not hit[(1 - hk) * group:(2 - hk) * group].any(), name
+
+
+# -------------------------------------------------------------- small norms ----
+
+@pytest.mark.parametrize("norm", [mxq.ROTARY_NORM_ROW, mxq.ROTARY_NORM_HEAD])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 2.0 ** -120])
+def test_rotary_norms_of_next_to_nothing(norm, eps):
+    """Rows of zeros and rows whose squares are subnormal, the smallest eps."""
+    say("small norms", norm, eps)
+    m, heads, kv, d = 40, 4, 2, 64
+    x = randn(gen(1), m, (heads + 2 * kv) * d).double() * torch.exp2(-torch.arange(m).double() - 50.0)[:, None]
+    x = x.to(BF16)
+    x[5] = 0
+    q, k = mxq.rotary_qkv(x.to(DEV), heads, kv, d, norm=norm, eps=eps)
+    want = rotary_want(x, heads, kv, d, torch.zeros(0, dtype=torch.float64), [], None, [torch.ones(d * (heads if norm == 1 else 1)),
+                                                                                         torch.ones(d * (kv if norm == 1 else 1))],
+                       norm, False, eps)
+    rotary_within(q, want[0], "q")
+    rotary_within(k, want[1], "k")
+    assert not q[5].any() and not k[5].any()
