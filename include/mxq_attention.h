@@ -119,7 +119,7 @@ int mxq_page_plan(const int32_t* cached, const int32_t* added, int32_t* block_ta
  *              freqs and axis are then not read)
  *   q_weight, k_weight  device bf16 [heads * head_dim], [kv_heads * head_dim] (row
  *              norm) or [head_dim] (head norm), null for ones; null without a norm
- *   eps        positive and finite with a norm
+ *   eps        at least 2^-126 and finite with a norm
  *   q          device bf16 [M][ldq] (output), null where heads is 0
  *   k          device bf16 [M][ldk] (output) or null
  *   cache      null for none; else k (after norm and rotation, of its bf16 values)
