@@ -68,20 +68,26 @@ __device__ __forceinline__ uint32_t head_max(uint32_t v, bool wide) {
   return wide ? umax(v, o) : v;
 }
 
-// 8 bf16 -> 8 E4M3 codes of a block with scale 2^(sb - 127), saturating at 448. (A NaN is kept:
-// the median of it and the two bounds would be a bound, and a key of -infinity drops out of
-// attention without a trace.)
+// 8 bf16 -> 8 E4M3 codes of a block with scale 2^(sb - 127), saturating at 448. A NaN is kept,
+// in a branch of its own: the median of it and the two bounds would be a bound, and a key of
+// -infinity drops out of attention without a trace. (Only a block that holds an infinity or a
+// NaN has a scale of 2^120. Without the branch: 58.3 us for 8195 rows of 40 + 8 + 8 heads, 57.7
+// so, 57.3 with the bounds alone.)
 __device__ __forceinline__ uint2 pack8_mxfp8(const uint4 c, uint32_t sb) {
-  float f[8];
+  float f[8], r[8];
   bf16x8_to_f32(c, f);
   const float inv = as_float((254u - sb) << 23);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = f[i] != f[i] ? f[i] : __builtin_amdgcn_fmed3f(f[i] * inv, -448.0f, 448.0f);
+  for (int i = 0; i < 8; ++i) r[i] = __builtin_amdgcn_fmed3f(f[i] * inv, -448.0f, 448.0f);
+  if (__any(sb >= 247u)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = f[i] != f[i] ? f[i] : r[i];
+  }
   uint2 o;
-  o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-  o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], (int)o.x, true);
-  o.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
-  o.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], (int)o.y, true);
+  o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
+  o.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], (int)o.x, true);
+  o.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], 0, false);
+  o.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[6], r[7], (int)o.y, true);
   return o;
 }
 
