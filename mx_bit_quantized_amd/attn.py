@@ -291,7 +291,8 @@ def attention(q, k, v, starts_q=None, starts_k=None, scale=None, window=(-1, -1)
     starts_q, starts_k: int32 [sequences + 1], the rows where sequences start and the last one ends; without them all rows are
     one sequence. A sequence's queries are the last of its positions; with ``window = (left, right)`` the one at p sees keys
     p - left .. p + right (-1: no limit, right 0: causal) and the first ``sinks`` ones up to p + right. Rows that see nothing
-    are zeros, rows of ``out`` behind the last sequence stay. scale: 1 / sqrt(D) by default. ``out`` may not overlap an input.
+    are zeros; rows of ``out`` behind the last sequence stay, which in an output that the call allocates means that they hold
+    anything. scale: 1 / sqrt(D) by default. ``out`` may not overlap an input.
     """
     dev = _index(q, "q")
     if q.dim() != 3 or k.dim() != 3:

@@ -25,14 +25,14 @@
 // sums, packing and maxima of tile t, fixed in place by scheduling barriers; operand
 // A is read from LDS eight fragments ahead, and a step has one barrier.
 //
-// 32760 x 32760, 40 heads of 128: 17.1 to 18 ms by the card, 1.22 to 1.29 PFLOP/s,
+// 32760 x 32760, 40 heads of 128: 17.1 to 18.4 ms by the card, 1.19 to 1.29 PFLOP/s,
 // against 1.41 to 1.65 PFLOP/s of large library products. There the MFMAs are busy
-// 73% of the cycles and the power cap holds the clock at 1.6 GHz (all-zero operands:
-// 12.95 ms). 65520 queries against 741 keys (6.5 tiles a workgroup): 667 us,
-// 0.83 PFLOP/s; of a workgroup's 28000 cycles 15500 are steps, 5700 the first
+// 73 to 74% of the cycles and the power cap holds the clock at 1.6 GHz (all-zero operands:
+// 12.95 ms). 65520 queries against 741 keys (6.5 tiles a workgroup): 656 to 684 us,
+// 0.81 to 0.84 PFLOP/s; of a workgroup's 28000 cycles 15500 are steps, 5700 the first
 // loads (rows of q from HBM, as the output's on their way there: 2.0 TB/s), 3300 the
 // first scores and the last product without their counterparts, 2800 the way out.
-// Causal prompts with a window of 1024: 330 us, 0.88 PFLOP/s, the same ends and the
+// Causal prompts with a window of 1024: 326 to 343 us, 0.88 PFLOP/s, the same ends and the
 // tiles that the window cuts (a fifth of them). Heads of 64, 296 rows, 30011 keys:
 // 37 us, 0.49 PFLOP/s: as many exponentials for half the products, 23% of the last
 // tile's rows empty, and the join (5 us).
@@ -718,6 +718,10 @@ static int64_t attention_slots(const mxq_attention_args& g) {
 // 16.6, 20.4; 37 x 30011, 64 + 8 heads of 64 n = 10, 21 (taken), 32: 39.8, 37.3, 39.7;
 // 100 x 4000, 40 + 40 of 128 n = 3, 6 (taken), 8, 16: 29.8, 25.5, 29.3, 36.4; 1000 x 1000,
 // 16 + 8 of 128 n = 1 (taken), 2, 4: 18.1, 22.5, 25.2.
+// The sequences' average length decides, and every sequence gets the same number: right for
+// lengths that are alike (64 sequences of 4 x 2547, 40 + 8 heads of 128, 160 us), not for one
+// long axis among many short ones, which one workgroup per key head and tile of rows then
+// walks: 4 x 100000 alone 87 us, among 63 of 4 x 1000 1770 us.
 static int attention_splits(const mxq_attention_args& g) {
   const int64_t items = attention_slots(g) * g.kv_heads;
   if (items == 0) return 1;

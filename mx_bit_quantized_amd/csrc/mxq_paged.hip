@@ -22,10 +22,13 @@
 //
 // One sequence of 131071, 40 + 8 heads of 128: 101 us, 5.3 TB/s (a copy: 4.9; a read
 // has no writes to turn the memory round for). 64 sequences, 262147 tokens in all, MXFP8:
-// 118 us, 4.7 TB/s. Both with the loads of a step issued before the arithmetic on the
+// 118 to 120 us, 4.7 TB/s. Both with the loads of a step issued before the arithmetic on the
 // step before: 102 and 124 us without. 9 sequences, window of 2048, heads of 64: 17.6 us
 // for 38 MB, 14 of them in this kernel: two steps a wave, so the chain of lengths,
-// table, keys, values and joins is what takes the time; then 3.5 us of join.
+// table, keys, values and joins is what takes the time; then 3.9 us of join.
+//
+// More than 16 query heads to a key head are pieces of their own, which read the cache
+// again: 32 sequences of 8000, one key head of 128, 16, 20, 33 query heads 33, 49, 67 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -18,8 +18,9 @@
 //
 // 75600 rows of 120 heads of 128, norm over the row, three axes: 620 us, 5.0 TB/s
 // (1754 us with loads where they are needed and a thread's 16 bytes 256 apart). 8195
-// rows of 56 heads, norm per head, into the cache and dense: 50 us, 5.0 TB/s. One
-// row: 3.3 us, 12 with the call.
+// rows of 56 heads, norm per head, into the cache and dense: 50 us, 5.0 TB/s; into the
+// cache alone 49 us, into an MXFP8 one 58, whose codes leave in pieces of 8 bytes and whose
+// scales leave as single bytes. One row: 3.3 us, 12 with the call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -388,8 +389,10 @@ hipError_t launch_rotary_qkv(const mxq_rotary_args& g, const mxq_kv_cache* cache
     a.mxfp8 = cache->format == MXQ_KV_MXFP8;
     a.units += g.kv_heads * per_head;
   }
-  // A row's sums need the whole row in one workgroup; heads on their own (or no norm) go to
-  // workgroups of 512 units.
+  // A row's sums need the whole row in one workgroup, which then holds up to four units a
+  // thread; heads on their own (or no norm) go to workgroups of 512 units. Two and four units
+  // spill registers: 4096 rows, row norm, 64 + 64 (one unit), 65 + 65, 128 + 128 (two), 170 +
+  // 170 heads of 128 (four) 49, 245, 327, 617 us.
   const bool row_norm = g.norm == MXQ_ROTARY_NORM_ROW;
   const int parts = row_norm ? 1 : (a.units + 511) / 512;
   const int units = (a.units + parts - 1) / parts;
