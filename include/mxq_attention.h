@@ -158,7 +158,7 @@ int mxq_rotary_qkv(const mxq_rotary_args* args, const mxq_kv_cache* cache, hipSt
  * is rounded to bf16 once. A row without visible keys is zeros, and so is one whose
  * scores are all -infinity. A row whose largest score (scale q . k) is past 7e8 in
  * magnitude, where fp32 holds no exponents any more, is NaN, and sums of weighted
- * values past fp32's range are infinities: MXQ_CHECK_FINITE reports both. Keys and
+ * values past fp32's range are infinities or NaN: MXQ_CHECK_FINITE reports all. Keys and
  * values at places that a query does not see may
  * hold anything. Rows of out behind the last sequence are left as they were.
  *   q, out     device bf16 [Mq][ldq], [Mq][ldo], heads * head_dim elements a row
